@@ -319,6 +319,145 @@ int wkv7_backward_noalloc(const void* r, const void* w_log, const void* k, const
                           void* da, void* db, float* ds0, int B, int T, int H, int D,
                           const int32_t* seq_offsets, int io_dtype, int w_dtype, void* stream);
 
+/*
+ * State-space layers: a short causal convolution, a selective scan (the sibling of
+ * the WKV recurrence with one decay per head and token and no removal term) and the
+ * group norm that reads out either recurrence.  "RWKV-7 Goose architecture analysis"
+ * sets the WKV state beside such scans (its comparison of RWKV, Mamba and RetNet); it
+ * prints no listing of them, so the formulas here are the operators' definitions.
+ *
+ * Differences from the conventions above, for these entry points only
+ *  - Activations are rows of a fixed width, one per token, at a row stride `ld_*` in
+ *    elements (ld >= width), so that column slices of a projection's output can be
+ *    passed without a copy.  Dense batches: row b T + t; packed batches (seq_offsets,
+ *    as in wkv7_forward): row t.  Rows of no sequence (before seq_offsets[0] or behind
+ *    seq_offsets[B]) are neither read for a result nor written; pairs of offsets that
+ *    are not monotone or leave [0, T] count as an empty sequence and set
+ *    WKV7_ERR_DEVICE_BOUNDS.
+ *  - Per-channel and per-head parameters and their gradients are fp32.
+ *  - Outputs and workspaces must be disjoint from the inputs and from each other,
+ *    except where a state may be updated in place.  Two row sets of one stride may
+ *    interleave (columns of one buffer).
+ *  - Sums, statistics, decays and states are fp32 or wider.
+ */
+typedef enum {
+    WKV7_ACT_NONE = 0, /* act(u) = u */
+    WKV7_ACT_SILU = 1  /* act(u) = u / (1 + exp(-u)) */
+} wkv7_act;
+
+/*
+ * wkv7_causal_conv — one filter of W taps per channel over the tokens of a sequence:
+ *
+ *     pre_t[c] = bias[c] + sum_{j < W} w[c][j] x_{t-W+1+j}[c],   y_t = act(pre_t)
+ *
+ * where the W - 1 rows before the first token are the sequence's state s0 (oldest
+ * first), or zeros.
+ *   x, y : rows of C channels.   w : [C][W], bias : [C] or NULL, fp32.
+ *   s0 : [B][W-1][C] in the io dtype, or NULL (zeros).
+ *   sT : [B][W-1][C], the last W - 1 rows of (s0, x), or NULL.  sT == s0 is allowed.
+ * W is 2, 3 or 4 (WKV7_ERR_UNSUPPORTED otherwise), any C >= 1.  T == 0: sT receives s0.
+ * wkv7_causal_conv_step: one token per sequence; x, y : B rows; s_in (NULL: zeros) is
+ * moved on by one row into s_out (which may be s_in).
+ * wkv7_causal_conv_backward: the gradient of <dy, y> + <dsT, sT>.
+ *   dsT : [B][W-1][C] in the io dtype, or NULL (zero);  dx : rows of C;
+ *   dw : [C][W];  dbias : [C] or NULL;  ds0 : [B][W-1][C] or NULL (not wanted).
+ *   workspace : at least wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, packed).
+ * The sums of dw and dbias are taken in a fixed order: equal calls give equal bits.
+ */
+int wkv7_causal_conv(const void* x, int64_t ld_x, const float* w, const float* bias, const void* s0, void* y,
+                     int64_t ld_y, void* sT, int B, int T, int C, int W, const int32_t* seq_offsets, int act,
+                     int io_dtype, void* stream);
+int wkv7_causal_conv_step(const void* x, int64_t ld_x, const float* w, const float* bias, const void* s_in, void* y,
+                          int64_t ld_y, void* s_out, int B, int C, int W, int act, int io_dtype, void* stream);
+size_t wkv7_causal_conv_backward_workspace_bytes(int B, int T, int C, int W, int packed);
+int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const float* bias, const void* s0,
+                              const void* dy, int64_t ld_dy, const void* dsT, void* dx, int64_t ld_dx, float* dw,
+                              float* dbias, void* ds0, void* workspace, size_t workspace_bytes, int B, int T, int C,
+                              int W, const int32_t* seq_offsets, int act, int io_dtype, void* stream);
+
+/*
+ * wkv7_selective_scan — per sequence and head, a state S of D x N (D = 64 rows of the
+ * head's channels, N columns):
+ *
+ *     delta_t = softplus(dt_t + dt_bias)   (dt_softplus = 0: delta_t = dt_t + dt_bias)
+ *     S_t = exp(A delta_t) S_{t-1} + delta_t x_t B_t^T
+ *     y_t = S_t C_t + D_skip x_t
+ *
+ *   x, y : rows of H heads x 64;  dt : rows of H in dt_dtype;  Bm, Cm : rows of G
+ *   groups x N, group g shared by the heads [g H / G, (g + 1) H / G).
+ *   A : [H];  D_skip, dt_bias : [H] or NULL (zeros), all fp32.
+ *   s0 : [B][H][64][N] fp32 or NULL (zeros);  sT : the same shape or NULL; sT == s0 is
+ *   allowed.  T == 0: sT receives s0.
+ *   workspace : at least wkv7_selective_scan_workspace_bytes(B, T, H, D, N, packed)
+ *   bytes, which is 0 (workspace may be NULL) when sequences and heads fill the GPU.
+ * D must be 64, N one of 16, 32, 64 and 128, G a divisor of H.  x, Bm, Cm and y need
+ * row strides of a multiple of 16 bytes; dt only the alignment of its elements.
+ * A dt of -inf leaves the state as it is (padding): x, Bm and Cm of such a token must
+ * still be finite.  Prompts are worked on in chunks of 64 tokens, so an infinity or
+ * NaN in x, Bm or Cm may reach the outputs of earlier tokens of its chunk.
+ * wkv7_selective_scan_step: one token per sequence, B rows; s_out may be s_in (NULL:
+ * zeros).
+ * wkv7_selective_scan_backward: the gradient of <dy, y> + <dsT, sT>.
+ *   dsT : [B][H][64][N] fp32 or NULL (zero).
+ *   dx : rows of H x 64;  ddt : rows of H in dt_dtype;  dB, dC : rows of G x N (summed
+ *   over a group's heads), in the io dtype; dx, dB and dC need the alignment of x.
+ *   dA : [H];  dD, ddt_bias : [H] or NULL (not wanted);  ds0 : [B][H][64][N] or NULL.
+ *   workspace : at least wkv7_selective_scan_backward_workspace_bytes(B, T, H, D, N, G,
+ *   io_dtype, packed) bytes (mostly the states and their gradients at every 64th
+ *   token).  Sums are taken in a fixed order: equal calls give equal bits.  T == 0: the
+ *   gradients of parameters are zero and ds0 receives dsT.
+ */
+size_t wkv7_selective_scan_workspace_bytes(int B, int T, int H, int D, int N, int packed);
+int wkv7_selective_scan(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt, const float* A, const void* Bm,
+                        int64_t ld_b, const void* Cm, int64_t ld_c, const float* D_skip, const float* dt_bias,
+                        const float* s0, void* y, int64_t ld_y, float* sT, void* workspace, size_t workspace_bytes,
+                        int B, int T, int H, int D, int N, int G, const int32_t* seq_offsets, int dt_softplus,
+                        int io_dtype, int dt_dtype, void* stream);
+int wkv7_selective_scan_step(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt, const float* A,
+                             const void* Bm, int64_t ld_b, const void* Cm, int64_t ld_c, const float* D_skip,
+                             const float* dt_bias, const float* s_in, void* y, int64_t ld_y, float* s_out, int B,
+                             int H, int D, int N, int G, int dt_softplus, int io_dtype, int dt_dtype, void* stream);
+size_t wkv7_selective_scan_backward_workspace_bytes(int B, int T, int H, int D, int N, int G, int io_dtype,
+                                                    int packed);
+int wkv7_selective_scan_backward(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt, const float* A,
+                                 const void* Bm, int64_t ld_b, const void* Cm, int64_t ld_c, const float* D_skip,
+                                 const float* dt_bias, const float* s0, const void* dy, int64_t ld_dy,
+                                 const float* dsT, void* dx, int64_t ld_dx, void* ddt, int64_t ld_ddt, float* dA,
+                                 void* dB, int64_t ld_db, void* dC, int64_t ld_dc, float* dD, float* ddt_bias,
+                                 float* ds0, void* workspace, size_t workspace_bytes, int B, int T, int H, int D,
+                                 int N, int G, const int32_t* seq_offsets, int dt_softplus, int io_dtype,
+                                 int dt_dtype, void* stream);
+
+/*
+ * wkv7_group_norm — over the L x C / G elements of sample n and group g of
+ * channels-last rows x [N][L][C]:
+ *
+ *     h = (x - mean) / sqrt(var + eps),   y = act(h weight[c] + bias[c])
+ *
+ * with the variance about the mean (divided by the count).  L = 1 normalises every row
+ * by itself: G = H heads is the per-head norm of a recurrence's read-out, G = 1 a layer
+ * norm.
+ *   x, y : N L rows of C;  weight, bias : [C] fp32 or NULL (ones, zeros).
+ *   stats : [N][G][2] fp32, mean and 1 / sqrt(var + eps), or NULL (not wanted).
+ *   workspace : at least wkv7_group_norm_workspace_bytes(N, L, C, G, io_dtype) bytes
+ *   (0 for most rows: workspace may then be NULL).
+ * G must divide C.  N == 0 or L == 0 is valid: nothing is written.
+ * wkv7_group_norm_backward: the gradient of <dy, y>; stats as the forward wrote them;
+ * dx : rows of C;  dweight, dbias : [C] or NULL (zeros when there are no rows).  Sums
+ * are taken in a fixed order.  workspace : wkv7_group_norm_backward_workspace_bytes.
+ * Samples are numbered in 16 bits where a group does not fit one block (L > 1, or
+ * more than 1024 vectors of channels in a row's group): N <= 65535 there.
+ */
+size_t wkv7_group_norm_workspace_bytes(int N, int L, int C, int G, int io_dtype);
+int wkv7_group_norm(const void* x, int64_t ld_x, const float* weight, const float* bias, void* y, int64_t ld_y,
+                    float* stats, void* workspace, size_t workspace_bytes, int N, int L, int C, int G, float eps,
+                    int act, int io_dtype, void* stream);
+size_t wkv7_group_norm_backward_workspace_bytes(int N, int L, int C, int G, int io_dtype);
+int wkv7_group_norm_backward(const void* x, int64_t ld_x, const float* weight, const float* bias, const float* stats,
+                             const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, int N, int L, int C, int G, int act,
+                             int io_dtype, void* stream);
+
 /* Human-readable text for a status code (static storage, never NULL). */
 const char* wkv7_status_string(int status);
 

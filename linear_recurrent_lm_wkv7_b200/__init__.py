@@ -18,10 +18,15 @@ from ._binding import (  # noqa: F401
     WKV7_BF16,
     WKV7_F32,
     Wkv7Error,
+    _code,
     _lib,
     wkv7_backward,
     wkv7_backward_noalloc,
     wkv7_backward_workspace_bytes,
+    wkv7_causal_conv,
+    wkv7_causal_conv_backward,
+    wkv7_causal_conv_backward_workspace_bytes,
+    wkv7_causal_conv_step,
     wkv7_debug_expire_wait,
     wkv7_decode_step,
     wkv7_decode_step_fused,
@@ -31,6 +36,15 @@ from ._binding import (  # noqa: F401
     wkv7_forward_long,
     wkv7_forward_long_workspace_bytes,
     wkv7_get_device_status,
+    wkv7_group_norm,
+    wkv7_group_norm_backward,
+    wkv7_group_norm_backward_workspace_bytes,
+    wkv7_group_norm_workspace_bytes,
+    wkv7_selective_scan,
+    wkv7_selective_scan_backward,
+    wkv7_selective_scan_backward_workspace_bytes,
+    wkv7_selective_scan_step,
+    wkv7_selective_scan_workspace_bytes,
     wkv7_state_apply,
     wkv7_state_map,
     wkv7_status_string,
@@ -243,3 +257,185 @@ def decode_step(r, w_log, k, v, a, b, state, y=None, stream=None):
         y = torch.empty_like(r)
     wkv7_decode_step(r, w_log, k, v, a, b, state, y, state, B, H, D, stream)
     return y
+
+
+# ---------------------------------------------------------------- state-space layers
+def _outputs(like, stream, inputs):
+    """The context in which outputs and workspaces of a call on ``stream`` are allocated:
+    that stream's, so that the allocator hands their memory on only in its order.  The
+    inputs are marked as used there."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), like.device)
+    for t in inputs:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes, device):
+    import torch
+
+    return torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device) if nbytes else None
+
+
+def _new(t, dtype=None):
+    """A contiguous tensor of the shape and device of ``t``."""
+    import torch
+
+    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
+
+
+def _rows(t, seq_offsets, inner):
+    """(B, T) of [B, T, ..] or of packed [T, ..] rows with ``inner`` more dimensions."""
+    want = inner + (1 if seq_offsets is not None else 2)
+    if t.dim() != want:
+        raise ValueError(f"expected {want} dimensions, not {t.dim()}")
+    if seq_offsets is not None:
+        return seq_offsets.numel() - 1, t.shape[0]
+    return t.shape[0], t.shape[1]
+
+
+def causal_conv(x, w, bias=None, s0=None, seq_offsets=None, act=None, want_state=True, stream=None):
+    """Short causal convolution over tokens, one filter per channel, with an activation
+    (``None`` or ``"silu"``).  ``x`` is [B, T, C], or packed [T, C] with int32
+    ``seq_offsets`` [B+1] on the device; its rows may be slices of wider ones.  ``w`` is
+    [C, W] fp32 with W of 2, 3 or 4, ``bias`` [C] fp32, ``s0`` [B, W-1, C] the rows before
+    the first token.  Returns ``(y, sT)``: ``sT`` [B, W-1, C] (None when ``want_state`` is
+    false) is the ``s0`` of the tokens that follow."""
+    B, T = _rows(x, seq_offsets, 1)
+    C, W = w.shape
+    with _outputs(x, stream, (x, w, bias, s0, seq_offsets)):
+        y = _new(x)
+        sT = x.new_empty((B, W - 1, C)) if want_state else None
+    wkv7_causal_conv(x, w, bias, s0, y, sT, B, T, C, W, seq_offsets, act, stream)
+    return y, sT
+
+
+def causal_conv_step(x, w, state, bias=None, act=None, y=None, stream=None):
+    """One token per sequence of ``causal_conv``: ``x`` [B, C], ``state`` [B, W-1, C]
+    updated in place.  Returns y ([B, C])."""
+    C, W = w.shape
+    if y is None:
+        with _outputs(x, stream, (x, w, state, bias)):
+            y = _new(x)
+    wkv7_causal_conv_step(x, w, bias, state, y, state, x.shape[0], C, W, act, stream)
+    return y
+
+
+def causal_conv_backward(x, w, dy, bias=None, s0=None, dsT=None, seq_offsets=None, act=None, workspace=None,
+                         stream=None):
+    """Gradient of <dy, y> + <dsT, sT> of ``causal_conv``.  Returns ``(dx, dw, dbias, ds0)``
+    (``dbias`` is None without ``bias``)."""
+    B, T = _rows(x, seq_offsets, 1)
+    C, W = w.shape
+    with _outputs(x, stream, (x, w, dy, bias, s0, dsT, seq_offsets, workspace)):
+        if workspace is None:
+            workspace = _scratch(wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, seq_offsets is not None),
+                                 x.device)
+        dx, dw = _new(x), _new(w)
+        dbias = _new(bias) if bias is not None else None
+        ds0 = x.new_empty((B, W - 1, C))
+    wkv7_causal_conv_backward(x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, workspace, B, T, C, W, seq_offsets, act,
+                              stream)
+    return dx, dw, dbias, ds0
+
+
+def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, s0=None, seq_offsets=None, dt_softplus=True,
+                   want_state=True, workspace=None, stream=None):
+    """Selective state-space scan S_t = exp(A delta_t) S_{t-1} + delta_t x_t B_t^T,
+    y_t = S_t C_t + D x_t with delta_t = softplus(dt_t + dt_bias).  ``x`` is [B, T, H, 64],
+    ``dt`` [B, T, H], ``Bm`` and ``Cm`` [B, T, G, N] (N of 16, 32, 64 or 128; G divides H), or
+    all packed along [T, ..] with int32 ``seq_offsets`` [B+1]; rows may be slices of wider
+    ones.  ``A``, ``D`` and ``dt_bias`` are [H] fp32, ``s0`` [B, H, 64, N] fp32.
+    ``workspace`` (a device tensor of at least ``wkv7_selective_scan_workspace_bytes``
+    bytes) is allocated when not given.  Returns ``(y, sT)`` like ``forward``."""
+    B, T = _rows(x, seq_offsets, 2)
+    H, P = x.shape[-2:]
+    G, N = Bm.shape[-2:]
+    with _outputs(x, stream, (x, dt, A, Bm, Cm, D, dt_bias, s0, seq_offsets, workspace)):
+        if workspace is None:
+            workspace = _scratch(wkv7_selective_scan_workspace_bytes(B, T, H, P, N, seq_offsets is not None),
+                                 x.device)
+        y = _new(x)
+        sT = A.new_empty((B, H, P, N)) if want_state else None
+    wkv7_selective_scan(x, dt, A, Bm, Cm, D, dt_bias, s0, y, sT, workspace, B, T, H, P, N, G, seq_offsets,
+                        dt_softplus, stream)
+    return y, sT
+
+
+def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, dt_softplus=True, y=None, stream=None):
+    """One token per sequence of ``selective_scan``: ``x`` [B, H, 64], ``dt`` [B, H], ``Bm``
+    and ``Cm`` [B, G, N], ``state`` [B, H, 64, N] fp32 updated in place.  Returns y
+    ([B, H, 64])."""
+    B, H, P = x.shape
+    G, N = Bm.shape[-2:]
+    if y is None:
+        with _outputs(x, stream, (x, dt, A, Bm, Cm, state, D, dt_bias)):
+            y = _new(x)
+    wkv7_selective_scan_step(x, dt, A, Bm, Cm, D, dt_bias, state, y, state, B, H, P, N, G, dt_softplus, stream)
+    return y
+
+
+def selective_scan_backward(x, dt, A, Bm, Cm, dy, D=None, dt_bias=None, s0=None, dsT=None, seq_offsets=None,
+                            dt_softplus=True, workspace=None, stream=None):
+    """Gradient of <dy, y> + <dsT, sT> of ``selective_scan``.  Returns ``(dx, ddt, dA, dB, dC,
+    dD, ddt_bias, ds0)`` (None for a parameter that was not given).
+    ``wkv7_selective_scan_backward`` takes outputs of the caller, which may be slices of
+    wider rows."""
+    B, T = _rows(x, seq_offsets, 2)
+    H, P = x.shape[-2:]
+    G, N = Bm.shape[-2:]
+    with _outputs(x, stream, (x, dt, A, Bm, Cm, dy, D, dt_bias, s0, dsT, seq_offsets, workspace)):
+        if workspace is None:
+            workspace = _scratch(
+                wkv7_selective_scan_backward_workspace_bytes(B, T, H, P, N, G, _code(x), seq_offsets is not None),
+                x.device)
+        dx, ddt, dA, dB, dC = (_new(t) for t in (x, dt, A, Bm, Cm))
+        dD = _new(D) if D is not None else None
+        dbias = _new(dt_bias) if dt_bias is not None else None
+        ds0 = A.new_empty((B, H, P, N))
+    wkv7_selective_scan_backward(x, dt, A, Bm, Cm, D, dt_bias, s0, dy, dsT, dx, ddt, dA, dB, dC, dD, dbias, ds0,
+                                 workspace, B, T, H, P, N, G, seq_offsets, dt_softplus, stream)
+    return dx, ddt, dA, dB, dC, dD, dbias, ds0
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=None, want_stats=False, workspace=None, stream=None):
+    """Group norm with an activation (``None`` or ``"silu"``) over channels-last rows: ``x``
+    [N, C] normalises the ``groups`` of every row (``groups`` = heads: the per-head norm of
+    a recurrence's read-out), [N, L, C] takes the statistics over the L rows of a sample
+    too.  ``weight`` and ``bias`` are [C] fp32.  Returns y, or ``(y, stats)`` with the
+    ``stats`` [N, groups, 2] that ``group_norm_backward`` takes."""
+    N, L, C = x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[-1])
+    with _outputs(x, stream, (x, weight, bias, workspace)):
+        if workspace is None:
+            workspace = _scratch(wkv7_group_norm_workspace_bytes(N, L, C, groups, _code(x)), x.device)
+        y = _new(x)
+        stats = _float32(x, (N, groups, 2)) if want_stats else None
+    wkv7_group_norm(x, weight, bias, y, stats, workspace, N, L, C, groups, eps, act, stream)
+    return (y, stats) if want_stats else y
+
+
+def group_norm_backward(x, groups, stats, dy, weight=None, bias=None, act=None, workspace=None, stream=None):
+    """Gradient of <dy, y> of ``group_norm``, from the statistics it returned.  Returns
+    ``(dx, dweight, dbias)`` (None for a parameter that was not given)."""
+    N, L, C = x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[-1])
+    with _outputs(x, stream, (x, stats, dy, weight, bias, workspace)):
+        if workspace is None:
+            workspace = _scratch(wkv7_group_norm_backward_workspace_bytes(N, L, C, groups, _code(x)), x.device)
+        dx = _new(x)
+        dw = _new(weight) if weight is not None else None
+        db = _new(bias) if bias is not None else None
+    wkv7_group_norm_backward(x, weight, bias, stats, dy, dx, dw, db, workspace, N, L, C, groups, act, stream)
+    return dx, dw, db
+
+
+def _float32(t, shape):
+    import torch
+
+    return torch.empty(shape, dtype=torch.float32, device=t.device)

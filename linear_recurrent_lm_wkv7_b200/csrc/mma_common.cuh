@@ -1,0 +1,141 @@
+// mma_common.cuh — warp-level bf16 products of the selective scan: fragments of
+// m16n8k16 with fp32 accumulation, fed by ldmatrix from padded shared-memory tiles.
+//
+// Values of more bits than bf16 are carried as a sum of bf16 planes, each the
+// rounding of what the planes before it left over: two planes hold 16 bits of
+// mantissa (relative error 2^-18), three hold 24.  A product of a P-plane by a
+// Q-plane value sums the plane products (i, j) with i + j < max(P, Q); what is left
+// out is below the last plane's rounding.
+//
+// Tiles: rows of `cols` bf16 at a pitch of cols + 8 elements.  The pitch is an odd
+// number of 16-byte chunks for cols a multiple of 16, so the eight rows that one
+// ldmatrix phase reads fall into different banks.
+#pragma once
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+
+namespace wkv7 {
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm2t(uint32_t addr, uint32_t r0, uint32_t r1) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(r0), "r"(r1)
+                 : "memory");
+}
+// 16-byte asynchronous copy, zero-filled when `full` is false (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+    const uint32_t n = full ? 16u : 0u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two floats as bf16 planes: plane k holds the pair's k-th rounding, `lo` in the low half.
+template <int P>
+__device__ __forceinline__ void split_pair(uint32_t (&r)[P], float lo, float hi) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        uint32_t u;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+        r[k] = u;
+        if (k + 1 < P) {
+            lo -= __uint_as_float(u << 16);
+            hi -= __uint_as_float(u & 0xffff0000u);
+        }
+    }
+}
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// d += a b over the planes of both.
+template <int PA, int PB>
+__device__ __forceinline__ void mma_planes(float (&d)[4], const uint32_t (&a)[PA][4], const uint32_t (&b)[PB][2]) {
+    constexpr int top = PA > PB ? PA : PB;
+#pragma unroll
+    for (int i = 0; i < PA; ++i)
+#pragma unroll
+        for (int j = 0; j < PB; ++j)
+            if (i + j < top) mma16816(d, a[i], b[j][0], b[j][1]);
+}
+
+// A tile in shared memory: PLANES x ROWS x COLS.
+template <int PLANES, int ROWS, int COLS>
+struct Tile {
+    static constexpr int pitch = (COLS + 8) * 2;  // bytes
+    static constexpr int plane = ROWS * pitch;
+    static constexpr int bytes = PLANES * plane;
+    static constexpr int planes = PLANES;
+};
+
+// Lane addresses of the four 8x8 blocks of a 16 x 16 piece at (row, col) of a tile:
+// blocks in the order (0,0) (8,0) (0,8) (8,8) of (row, col): the A fragment of a
+// row-major A, or with `t` (transposing load) of an A stored [k][m], where row is k.
+template <typename TL>
+__device__ __forceinline__ uint32_t addr_a(uint32_t base, int row, int col, int lane) {
+    return base + (row + (lane & 15)) * TL::pitch + (col + (lane >> 4) * 8) * 2;
+}
+// Order (0,0) (0,8) (8,0) (8,8): two n-tiles' B fragments (k 0-7 and 8-15 of rows
+// n 0-7, then of rows n 8-15) from a B stored [n][k].
+template <typename TL>
+__device__ __forceinline__ uint32_t addr_b(uint32_t base, int row, int col, int lane) {
+    return base + (row + (lane & 7) + (lane >> 4) * 8) * TL::pitch + (col + ((lane >> 3) & 1) * 8) * 2;
+}
+
+// A fragments [m 16][k 16] of a tile stored [m][k].
+template <typename TL>
+__device__ __forceinline__ void frag_a(uint32_t (&f)[TL::planes][4], uint32_t base, int m, int k, int lane) {
+#pragma unroll
+    for (int p = 0; p < TL::planes; ++p) ldsm4(f[p], addr_a<TL>(base + p * TL::plane, m, k, lane));
+}
+// The same of a tile stored [k][m].
+template <typename TL>
+__device__ __forceinline__ void frag_a_t(uint32_t (&f)[TL::planes][4], uint32_t base, int m, int k, int lane) {
+#pragma unroll
+    for (int p = 0; p < TL::planes; ++p) {
+        uint32_t r[4];  // (k 0-7, m 0-7), (k 8-15, m 0-7), (k 0-7, m 8-15), (k 8-15, m 8-15)
+        ldsm4t(r, addr_a<TL>(base + p * TL::plane, k, m, lane));
+        f[p][0] = r[0], f[p][1] = r[2], f[p][2] = r[1], f[p][3] = r[3];
+    }
+}
+// B fragments of two n-tiles [n 16][k 16] of a tile stored [n][k]: f[tile][plane][2].
+template <typename TL>
+__device__ __forceinline__ void frag_b(uint32_t (&f)[2][TL::planes][2], uint32_t base, int n, int k, int lane) {
+#pragma unroll
+    for (int p = 0; p < TL::planes; ++p) {
+        uint32_t r[4];
+        ldsm4(r, addr_b<TL>(base + p * TL::plane, n, k, lane));
+        f[0][p][0] = r[0], f[0][p][1] = r[1], f[1][p][0] = r[2], f[1][p][1] = r[3];
+    }
+}
+// The same of a tile stored [k][n].
+template <typename TL>
+__device__ __forceinline__ void frag_b_t(uint32_t (&f)[2][TL::planes][2], uint32_t base, int n, int k, int lane) {
+#pragma unroll
+    for (int p = 0; p < TL::planes; ++p) {
+        uint32_t r[4];  // (k 0-7, n 0-7), (k 8-15, n 0-7), (k 0-7, n 8-15), (k 8-15, n 8-15)
+        ldsm4t(r, addr_a<TL>(base + p * TL::plane, k, n, lane));
+        f[0][p][0] = r[0], f[0][p][1] = r[1], f[1][p][0] = r[2], f[1][p][1] = r[3];
+    }
+}
+
+}  // namespace wkv7

@@ -1,0 +1,191 @@
+// scan_common.cuh — what the selective scan's forward and backward share: the cut
+// into sequences, segments and chunks, the per-chunk decays, and the tile loads.
+//
+//   delta_t = softplus(dt_t + dt_bias) (or dt_t + dt_bias),   a_t = exp(A delta_t)
+//   S_t = a_t S_{t-1} + delta_t x_t B_t^T  (64 x N per head),   y_t = S_t C_t + D x_t
+//
+// With l_t = sum_{i<=t} A delta_i from the start of a chunk of 64 tokens and S_0 the
+// state there:
+//   y_t = sum_{s<=t} exp(l_t - l_s) (C_t . B_s) delta_s x_s + exp(l_t) S_0 C_t + D x_t
+//   S_64 = exp(l_64) S_0 + sum_s exp(l_64 - l_s) delta_s x_s B_s^T
+// Only differences l_t - l_s with s <= t are exponentiated, so nothing overflows that
+// the recurrence itself would not.  l is summed in 64 bits and kept as two floats:
+// behind strong decays (|l| of thousands) the difference of two neighbours still
+// has 32 bits.
+#pragma once
+#include "mma_common.cuh"
+#include "seq_common.cuh"
+
+namespace wkv7 {
+
+constexpr int kChunk = 64;   // tokens per chunk
+constexpr int kScanP = kHead;  // rows of the state
+constexpr int kScanThreads = 256;
+
+// Planes of an input; of fp32 values that only go into outputs of the io type (two
+// leave an error of 2^-18, far below the rounding to bf16); of those that go into
+// states and sums that stay fp32 (two left errors of 3e-6 in states, and of 2e-5 in dA
+// where its terms cancel).
+template <typename IO>
+constexpr int kInPlanes = sizeof(IO) == 2 ? 1 : 3;
+template <typename IO>
+constexpr int kCalcPlanes = sizeof(IO) == 2 ? 2 : 3;
+constexpr int kStatePlanes = 3;
+
+// How sequences are cut into segments of `seg` tokens (a multiple of 64): dense ones
+// into spb = ceil(T / seg) slots each; packed ones own the slots from
+// offs[n] / seg + n on, which are at least as many as they need and end at
+// T / seg + B at the latest.
+struct SegMap {
+    const int32_t* offs;
+    int B, T;
+    long seg;
+    int spb;
+};
+inline __host__ __device__ long seg_slots(const SegMap& m) {
+    return m.offs ? m.T / m.seg + m.B : static_cast<long>(m.B) * m.spb;
+}
+// The cut that the scan uses for a problem (wkv7_scan.cu): one segment per sequence
+// (seg >= T) where sequences and heads fill the device.
+SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed);
+__device__ __forceinline__ long seg_first(const SegMap& m, int n, long lo) {
+    return m.offs ? lo / m.seg + n : static_cast<long>(n) * m.spb;
+}
+// Sequence n and rows [r0, r1) of a slot; false when the slot is not in use.
+__device__ __forceinline__ bool seg_rows(const SegMap& m, long slot, int& n, long& r0, long& r1, long& lo, long& hi,
+                                         int* status) {
+    if (m.offs) {
+        int a = 0, b = m.B - 1;  // the largest n whose first slot is not behind this one
+        while (a < b) {
+            const int c = (a + b + 1) >> 1;
+            if (m.offs[c] / m.seg + c <= slot)
+                a = c;
+            else
+                b = c - 1;
+        }
+        n = a;
+    } else {
+        n = static_cast<int>(slot / m.spb);
+    }
+    seq_span(m.offs, n, m.T, lo, hi, status);
+    r0 = lo + (slot - seg_first(m, n, lo)) * m.seg;
+    r1 = r0 + m.seg < hi ? r0 + m.seg : hi;
+    return r0 >= lo && r0 < hi;
+}
+
+// ---------------------------------------------------------------- decays
+__device__ __forceinline__ float softplus_f32(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// Per token of a chunk, in shared memory.  hi + lo = l_t log2(e).
+struct Decays {
+    float delta[kChunk];  // 0 past the end
+    float hi[kChunk], lo[kChunk];
+    float from[kChunk];   // exp(l_t): from the chunk's start to t
+    float to[kChunk];     // exp(l_64 - l_t): from t to the chunk's end
+    float total;          // exp(l_64)
+    float pad[3];
+};
+// exp(l_t - l_s)
+__device__ __forceinline__ float decay_between(const Decays& d, int t, int s) {
+    return ex2_ftz((d.hi[t] - d.hi[s]) + (d.lo[t] - d.lo[s]));
+}
+
+// 2^v for a 64-bit exponent: the part below the float's last place as a factor.
+__device__ __forceinline__ float exp2_f64(double v) {
+    const float h = static_cast<float>(v);
+    return ex2_ftz(h) * fmaf(static_cast<float>(v - h), 0.69314718f, 1.f);
+}
+
+// One warp: the decays of the chunk whose raw dt values lane l holds for tokens 2 l
+// and 2 l + 1 (`n` of them exist).
+__device__ __forceinline__ void chunk_decays(Decays& d, float dt0, float dt1, int n, float A, float bias,
+                                             bool softplus, int lane) {
+    float e0 = dt0 + bias, e1 = dt1 + bias;
+    if (softplus) {
+        e0 = softplus_f32(e0);
+        e1 = softplus_f32(e1);
+    }
+    if (2 * lane >= n) e0 = 0.f;
+    if (2 * lane + 1 >= n) e1 = 0.f;
+    constexpr double kLog2e = 1.4426950408889634074;
+    const double s = static_cast<double>(A) * kLog2e;
+    const double l0 = e0 * s;
+    double l1 = l0 + e1 * s;
+    double run = l1;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, run, m);
+        if (lane >= m) run += o;
+    }
+    double before = __shfl_up_sync(0xffffffffu, run, 1);
+    if (lane == 0) before = 0.0;
+    const double c0 = before + l0, c1 = before + l1;
+    const double end = __shfl_sync(0xffffffffu, run, 31);
+    const float h0 = static_cast<float>(c0), h1 = static_cast<float>(c1);
+    *reinterpret_cast<float2*>(&d.delta[2 * lane]) = make_float2(e0, e1);
+    *reinterpret_cast<float2*>(&d.hi[2 * lane]) = make_float2(h0, h1);
+    *reinterpret_cast<float2*>(&d.lo[2 * lane]) =
+        make_float2(static_cast<float>(c0 - h0), static_cast<float>(c1 - h1));
+    *reinterpret_cast<float2*>(&d.from[2 * lane]) = make_float2(exp2_f64(c0), exp2_f64(c1));
+    *reinterpret_cast<float2*>(&d.to[2 * lane]) = make_float2(exp2_f64(end - c0), exp2_f64(end - c1));
+    if (lane == 31) d.total = exp2_f64(end);
+}
+
+// ---------------------------------------------------------------- tile loads
+// Rows [0, 64) x COLS of a chunk into a tile: row r from src + r * ld while r < n,
+// zeros behind.  bf16: asynchronous copies.  fp32: split into planes on the way.
+template <typename TL, int COLS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, long ld, int n, int tid,
+                                          int threads) {
+    constexpr int per = COLS / 8;
+    for (int i = tid; i < kChunk * per; i += threads) {
+        const int r = i / per, c = i % per;
+        cp_async16(dst + r * TL::pitch + c * 16, src + (r < n ? r * ld : 0) + c * 8, r < n);
+    }
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+template <typename TL, int COLS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const float* src, long ld, int n, int tid, int threads) {
+    constexpr int per = COLS / 4;
+    for (int i = tid; i < kChunk * per; i += threads) {
+        const int r = i / per, c = i % per;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) v = *reinterpret_cast<const float4*>(src + r * ld + c * 4);
+        uint32_t a[TL::planes], b[TL::planes];
+        split_pair<TL::planes>(a, v.x, v.y);
+        split_pair<TL::planes>(b, v.z, v.w);
+#pragma unroll
+        for (int p = 0; p < TL::planes; ++p) sts64(dst + p * TL::plane + r * TL::pitch + c * 8, a[p], b[p]);
+    }
+}
+
+__device__ __forceinline__ float load_dt(const void* dt, long i, bool bf16) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(dt)[i]) : static_cast<const float*>(dt)[i];
+}
+
+// The scaled transpose of x as planes: value pairs of an A fragment (tile stored
+// [s][p]) times the two tokens' factors.
+template <int PIN, int POUT>
+__device__ __forceinline__ void scale_frag(uint32_t (&out)[POUT][4], const uint32_t (&in)[PIN][4], float f0, float f1,
+                                           float f8, float f9) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float lo = 0.f, hi = 0.f;
+#pragma unroll
+        for (int p = PIN - 1; p >= 0; --p) {
+            lo += bf_lo(in[p][r]);
+            hi += bf_hi(in[p][r]);
+        }
+        uint32_t u[POUT];
+        split_pair<POUT>(u, lo * (r < 2 ? f0 : f8), hi * (r < 2 ? f1 : f9));
+#pragma unroll
+        for (int p = 0; p < POUT; ++p) out[p][r] = u[p];
+    }
+}
+
+}  // namespace wkv7

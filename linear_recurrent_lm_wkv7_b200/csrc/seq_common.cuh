@@ -1,0 +1,122 @@
+// seq_common.cuh — what the causal convolution, the selective scan and the group
+// norm share: 16-byte vectors of either storage type, the activation and its
+// derivative, and the walk over packed sequences.
+#pragma once
+#include "wkv7_internal.cuh"
+
+namespace wkv7 {
+
+// ---------------------------------------------------------------- vectors
+// VEC consecutive elements as floats, in accesses of 8 or 16 bytes (VEC = 4 or 8,
+// the address aligned to VEC elements) or element by element (VEC = 1).
+template <int VEC>
+__device__ __forceinline__ void load_vec(float (&f)[VEC], const __nv_bfloat16* p) {
+    if constexpr (VEC == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else if constexpr (VEC == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        f[0] = __uint_as_float(u.x << 16), f[1] = __uint_as_float(u.x & 0xffff0000u);
+        f[2] = __uint_as_float(u.y << 16), f[3] = __uint_as_float(u.y & 0xffff0000u);
+    } else {
+        static_assert(VEC == 1, "8, 4 or 1 bf16");
+        f[0] = __bfloat162float(*p);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void load_vec(float (&f)[VEC], const float* p) {
+    if constexpr (VEC == 8) {
+        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+    } else if constexpr (VEC == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p);
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+    } else {
+        static_assert(VEC == 1, "8, 4 or 1 fp32");
+        f[0] = *p;
+    }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[VEC]) {
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                  pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    } else if constexpr (VEC == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+    } else {
+        static_assert(VEC == 1, "8, 4 or 1 bf16");
+        *p = __float2bfloat16_rn(f[0]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&f)[VEC]) {
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else if constexpr (VEC == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+        static_assert(VEC == 1, "8, 4 or 1 fp32");
+        *p = f[0];
+    }
+}
+// elements of a 16-byte vector
+template <typename IO>
+constexpr int kVec = 16 / static_cast<int>(sizeof(IO));
+
+// ---------------------------------------------------------------- activation
+// 1 / (1 + exp(-x)).  exp(-x) overflows to +inf below x = -88, where the quotient
+// is 0, its limit.
+__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float act_f32(float x, int act) { return act == WKV7_ACT_SILU ? x * sigmoid_f32(x) : x; }
+// d act(x) / dx
+__device__ __forceinline__ float act_grad_f32(float x, int act) {
+    if (act != WKV7_ACT_SILU) return 1.f;
+    const float s = sigmoid_f32(x);
+    return s * (1.f + x * (1.f - s));
+}
+
+// ---------------------------------------------------------------- packed sequences
+// Start and end row of sequence n of B.  `offs` null: dense sequences of T rows.
+// Packed offsets that are not monotone or leave [0, T] give an empty sequence and
+// set WKV7_ERR_DEVICE_BOUNDS, so that no row outside the tensors is ever addressed.
+__device__ __forceinline__ void seq_span(const int32_t* offs, int n, int T, long& lo, long& hi, int* status) {
+    if (!offs) {
+        lo = static_cast<long>(n) * T;
+        hi = lo + T;
+        return;
+    }
+    lo = offs[n];
+    hi = offs[n + 1];
+    if (lo < 0 || hi < lo || hi > T) {
+        report_status(status, WKV7_ERR_DEVICE_BOUNDS);
+        hi = lo = 0;
+    }
+}
+
+// The sequence that owns packed row `row`: the largest n in [0, B) with
+// offs[n] <= row (sequences of no tokens share their offset with the next one and
+// are passed over).  The caller checks that row < offs[n + 1].
+__device__ __forceinline__ int seq_of_row(const int32_t* offs, int B, long row) {
+    int a = 0, b = B - 1;
+    while (a < b) {
+        const int m = (a + b + 1) >> 1;
+        if (offs[m] <= row)
+            a = m;
+        else
+            b = m - 1;
+    }
+    return a;
+}
+
+}  // namespace wkv7

@@ -69,6 +69,18 @@ __global__ void copy_or_zero_states(const float* __restrict__ s0, float* __restr
 
 }  // namespace
 
+namespace wkv7 {
+
+int device_check() { return cached_device_check(); }
+int device_status_word(int** out) { return status_ptr(out); }
+cudaError_t launch_copy_states(const float* s0, float* sT, long n, cudaStream_t stream) {
+    const int blocks = static_cast<int>((n + 255) / 256 < 1184 ? (n + 255) / 256 : 1184);
+    copy_or_zero_states<<<blocks, 256, 0, stream>>>(s0, sT, n);
+    return cudaGetLastError();
+}
+
+}  // namespace wkv7
+
 extern "C" {
 
 int wkv7_version(void) { return 1 * 10000 + 0 * 100 + 0; }

@@ -93,6 +93,134 @@ struct BackwardArgs {
     int* status;
 };
 
+// ---- causal convolution (wkv7_conv.cu); ld*: elements between token rows
+struct ConvArgs {
+    const void* x;
+    long ldx;
+    const float *w, *bias;
+    const void* s0;
+    void* y;
+    long ldy;
+    void* sT;  // null: not wanted; s0: in place
+    int B, T, C, W;
+    const int32_t* seq_offsets;
+    int act;
+    int* status;
+};
+struct ConvBwdArgs {
+    const void* x;
+    long ldx;
+    const float *w, *bias;
+    const void *s0, *dy;
+    long lddy;
+    const void* dsT;
+    void* dx;
+    long lddx;
+    float *dw, *dbias;
+    void* ds0;
+    float* ws;
+    int B, T, C, W;
+    const int32_t* seq_offsets;
+    int act;
+    int* status;
+};
+cudaError_t launch_conv(const ConvArgs& p, int io_dtype, cudaStream_t stream);
+cudaError_t launch_conv_step(const ConvArgs& p, int io_dtype, cudaStream_t stream);
+long conv_bwd_blocks(long rows);
+size_t conv_bwd_workspace_floats(long rows, int C, int W);
+cudaError_t launch_conv_backward(const ConvBwdArgs& p, int io_dtype, cudaStream_t stream);
+
+// ---- selective scan (wkv7_scan.cu, wkv7_scan_backward.cu)
+struct ScanArgs {
+    const void* x;
+    long ldx;
+    const void* dt;
+    long lddt;
+    const float* A;
+    const void* Bm;
+    long ldb;
+    const void* Cm;
+    long ldc;
+    const float *D, *dt_bias, *s0;
+    void* y;
+    long ldy;
+    float *sT, *ws;
+    int B, T, H, N, G;
+    const int32_t* seq_offsets;
+    int softplus, dt_dtype;
+    int* status;
+};
+size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed);
+cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream);
+cudaError_t launch_scan_step(const ScanArgs& p, int io_dtype, cudaStream_t stream);
+
+struct ScanBwdArgs {
+    const void* x;
+    long ldx;
+    const void* dt;
+    long lddt;
+    const float* A;
+    const void* Bm;
+    long ldb;
+    const void* Cm;
+    long ldc;
+    const float *D, *dt_bias, *s0;
+    const void* dy;
+    long lddy;
+    const float* dsT;
+    void* dx;
+    long lddx;
+    void* ddt;
+    long ldddt;
+    float* dA;
+    void* dB;
+    long lddb;
+    void* dC;
+    long lddc;
+    float *dD, *ddt_bias, *ds0;
+    void* ws;
+    int B, T, H, N, G;
+    const int32_t* seq_offsets;
+    int softplus, dt_dtype;
+    int* status;
+};
+size_t scan_backward_workspace_bytes(int B, int T, int H, int N, int G, int io_dtype, bool packed);
+cudaError_t launch_scan_backward(const ScanBwdArgs& p, int io_dtype, cudaStream_t stream);
+
+// ---- group norm (wkv7_norm.cu)
+struct NormArgs {
+    const void* x;
+    long ldx;
+    const float *weight, *bias;
+    void* y;
+    long ldy;
+    float *stats, *ws;
+    int N, L, C, G;
+    float eps;
+    int act;
+};
+struct NormBwdArgs {
+    const void* x;
+    long ldx;
+    const float *weight, *bias, *stats;
+    const void* dy;
+    long lddy;
+    void* dx;
+    long lddx;
+    float *dw, *db, *ws;
+    int N, L, C, G;
+    int act;
+};
+size_t norm_workspace_floats(int N, int L, int C, int G, int io_dtype, bool backward);
+cudaError_t launch_norm(const NormArgs& p, int io_dtype, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormBwdArgs& p, int io_dtype, cudaStream_t stream);
+
+// ---- wkv7_api.cu, for the other files of entry points
+int device_check();               // WKV7_OK on an sm_100 device, else the status to return
+int device_status_word(int** out);  // the current device's status word
+// sT <- s0, or zeros, n floats (calls without tokens)
+cudaError_t launch_copy_states(const float* s0, float* sT, long n, cudaStream_t stream);
+
 cudaError_t launch_prefill(const PrefillArgs& p, int io_dtype, int w_dtype, cudaStream_t stream);
 // warp-specialised kernel for bf16 inputs (wkv7_prefill_pipe.cu)
 cudaError_t launch_prefill_pipe(const PrefillArgs& p, int w_dtype, cudaStream_t stream);

@@ -1,0 +1,659 @@
+// wkv7_norm.cu — group norm over channels-last rows, with an activation:
+//
+//   x [N][L][C], G groups of Cg = C / G neighbouring channels; over the L Cg elements
+//   of sample n and group g:  mean, var = mean((x - mean)^2), rstd = (var + eps)^-1/2
+//   h = (x - mean) rstd,   y = act(h weight[c] + bias[c])
+//
+// and its gradient.  With q = dy act'(h weight + bias):
+//   dbias = sum q,   dweight = sum q h   (over samples and rows)
+//   dx = rstd (q w - m1 - h m2),   m1 = mean(q w),  m2 = mean(q w h)  over the group
+//
+// A few operations per element: memory is the bound, and what matters is to read x
+// (and dy) once.  Two forms:
+//   row form   (L = 1 and a group that fits a team's registers): a team of up to 32
+//              lanes or a block holds the group, takes its mean, then the squares about
+//              the mean, and writes; everything is read once.
+//   split form (any other size): partial sums per (sample, split of the rows), joined
+//              by a second pass that writes y.  x is read twice, the second time from
+//              L2 where it fits.
+#include "seq_common.cuh"
+
+namespace wkv7 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ float rstd_of(float var, float eps) { return 1.f / sqrtf(var + eps); }
+
+// Sum over the team of TEAM threads (32 lanes or fewer: shuffles; 256: the block).
+// Every thread gets the same value.
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float* red) {
+    constexpr int LN = TEAM < 32 ? TEAM : 32;
+#pragma unroll
+    for (int m = LN / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(kFull, v, m);
+    if constexpr (TEAM > 32) {
+        __syncthreads();  // the previous sum has been read
+        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TEAM / 32; ++i) v += red[i];
+    }
+    return v;
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_param(float (&f)[VEC], const float* p, int c, float none) {
+    if (p) {
+        load_vec<VEC>(f, p + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = none;
+    }
+}
+
+// ---------------------------------------------------------------- row form
+// Unit u = row * G + group.  A team's lane holds vectors lane, lane + TEAM, .. of the
+// group: K of them.
+template <typename IO, int VEC, int TEAM, int K>
+__global__ void __launch_bounds__(kThreads)
+    norm_row_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
+                    const float* __restrict__ bias, IO* __restrict__ y, long ldy, float* __restrict__ stats,
+                    long units, int G, int Cg, float eps, int act) {
+    __shared__ float red[TEAM > 32 ? TEAM / 32 : 1];
+    const int lane = threadIdx.x % TEAM;
+    const long u = static_cast<long>(blockIdx.x) * (kThreads / TEAM) + threadIdx.x / TEAM;
+    const bool live = u < units;  // a whole team is live or not; teams past the end still take part in shuffles
+    const long row = live ? u / G : 0;
+    const int g = live ? static_cast<int>(u % G) : 0;
+    const int nv = Cg / VEC;
+    float v[K][VEC];
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = lane + k * TEAM;
+        if (live && i < nv) {
+            load_vec<VEC>(v[k], x + row * ldx + static_cast<long>(g) * Cg + i * VEC);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += v[k][e];
+        }
+    }
+    const float mean = team_sum<TEAM>(s, red) / Cg;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (live && lane + k * TEAM < nv)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                v[k][e] -= mean;
+                s = fmaf(v[k][e], v[k][e], s);
+            }
+    const float rstd = rstd_of(team_sum<TEAM>(s, red) / Cg, eps);
+    if (!live) return;
+    if (stats && lane == 0) {
+        stats[2 * u] = mean;
+        stats[2 * u + 1] = rstd;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = lane + k * TEAM;
+        if (i >= nv) continue;
+        const int c = g * Cg + i * VEC;
+        float wv[VEC], bv[VEC], out[VEC];
+        load_param<VEC>(wv, weight, c, 1.f);
+        load_param<VEC>(bv, bias, c, 0.f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = act_f32(fmaf(v[k][e] * rstd, wv[e], bv[e]), act);
+        store_vec<VEC>(y + row * ldy + c, out);
+    }
+}
+
+// The backward keeps a team on one group and walks rows, so that the sums of dweight
+// and dbias over the rows stay in registers.  Block (bx, by): groups bx * gpb ..,
+// rows by * rpb + team row, in steps of gridDim.y * rpb; gpb * rpb teams in the block.
+// The block's sums go to part [by][2][C].
+template <typename IO, int VEC, int TEAM, int K>
+__global__ void __launch_bounds__(kThreads)
+    norm_row_bwd_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
+                        const float* __restrict__ bias, const float* __restrict__ stats, const IO* __restrict__ dy,
+                        long lddy, IO* __restrict__ dx, long lddx, float* __restrict__ part, long N, int G, int Cg,
+                        int gpb, int act) {
+    constexpr int TEAMS = kThreads / TEAM;
+    __shared__ float red[TEAM > 32 ? TEAM / 32 : 1];
+    __shared__ float sums[kThreads * VEC];
+    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+    const int rpb = TEAMS / gpb;
+    const int g = blockIdx.x * gpb + team % gpb, trow = team / gpb;
+    const bool member = trow < rpb && g < G;
+    const int nv = Cg / VEC;
+    float wv[K][VEC], bv[K][VEC], aw[K][VEC], ab[K][VEC];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = lane + k * TEAM;
+        if (member && i < nv) {
+            load_param<VEC>(wv[k], weight, g * Cg + i * VEC, 1.f);
+            load_param<VEC>(bv[k], bias, g * Cg + i * VEC, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) aw[k][e] = ab[k][e] = 0.f;
+    }
+    const long step = static_cast<long>(gridDim.y) * rpb;
+    // every thread of the block takes the same number of turns: team_sum is collective
+    for (long r0 = static_cast<long>(blockIdx.y) * rpb; r0 < N; r0 += step) {
+        const long row = r0 + trow;
+        const bool live = member && row < N;
+        float mean = 0.f, rstd = 0.f, h[K][VEC], q[K][VEC], s1 = 0.f, s2 = 0.f;
+        if (live) {
+            mean = stats[2 * (row * G + g)];
+            rstd = stats[2 * (row * G + g) + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int i = lane + k * TEAM;
+            if (!live || i >= nv) continue;
+            const int c = g * Cg + i * VEC;
+            load_vec<VEC>(h[k], x + row * ldx + c);
+            load_vec<VEC>(q[k], dy + row * lddy + c);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                h[k][e] = (h[k][e] - mean) * rstd;
+                q[k][e] *= act_grad_f32(fmaf(h[k][e], wv[k][e], bv[k][e]), act);
+                ab[k][e] += q[k][e];
+                aw[k][e] = fmaf(q[k][e], h[k][e], aw[k][e]);
+                q[k][e] *= wv[k][e];
+                s1 += q[k][e];
+                s2 = fmaf(q[k][e], h[k][e], s2);
+            }
+        }
+        const float m1 = team_sum<TEAM>(s1, red) / Cg;
+        const float m2 = team_sum<TEAM>(s2, red) / Cg;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int i = lane + k * TEAM;
+            if (!live || i >= nv) continue;
+            float d[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) d[e] = rstd * (q[k][e] - m1 - h[k][e] * m2);
+            store_vec<VEC>(dx + row * lddx + static_cast<long>(g) * Cg + i * VEC, d);
+        }
+    }
+    // the block's sums: team rows in order
+    const long C = static_cast<long>(G) * Cg;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sums[threadIdx.x * VEC + e] = which ? ab[k][e] : aw[k][e];
+            __syncthreads();
+            const int i = lane + k * TEAM;
+            if (trow != 0 || !member || i >= nv) continue;
+            float s[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[e] = 0.f;
+            for (int t = 0; t < rpb; ++t)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s[e] += sums[((t * gpb + team) * TEAM + lane) * VEC + e];
+            store_vec<VEC>(part + (static_cast<long>(blockIdx.y) * 2 + which) * C + g * Cg + i * VEC, s);
+        }
+}
+
+// out [2][C] = dweight, dbias: the partials [nblk][2][C] added in the order of the blocks.
+__global__ void __launch_bounds__(kThreads)
+    norm_sum_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db, long nblk,
+                    long C) {
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x % 32, sub = threadIdx.x / 32;
+    const long col = static_cast<long>(blockIdx.x) * 32 + lane;
+    float s = 0.f;
+    if (col < 2 * C)
+        for (long b = sub; b < nblk; b += 8) s += part[b * 2 * C + col];
+    red[sub][lane] = s;
+    __syncthreads();
+    if (sub != 0 || col >= 2 * C) return;
+    s = 0.f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) s += red[t][lane];
+    float* dst = col < C ? dw : db;
+    if (dst) dst[col < C ? col : col - C] = s;
+}
+
+// ---------------------------------------------------------------- split form
+// (count, mean, sum of squares about the mean) of a set of values
+struct Moments {
+    float n, mean, m2;
+};
+// Of the union of two sets.  No difference of large sums: safe for any mean.
+__device__ __forceinline__ Moments merge(const Moments& a, const Moments& b) {
+    const float n = a.n + b.n;
+    if (n == 0.f) return a;
+    const float d = b.mean - a.mean, f = b.n / n;
+    return {n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
+}
+
+// Block (split, sample, tile of 256 vectors of channels).  Thread: one vector, every
+// `par`-th row of the split.
+template <typename IO, int VEC>
+__global__ void __launch_bounds__(kThreads)
+    norm_stats_kernel(const IO* __restrict__ x, long ldx, float* __restrict__ part, long L, int C, int Cg, int lanes,
+                      long split_rows) {
+    __shared__ Moments mom[kThreads];
+    const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
+    const int c0 = blockIdx.z * lanes * VEC, c = c0 + lane * VEC;
+    const bool member = prow < par && c < C;
+    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
+    const IO* base = x + static_cast<long>(blockIdx.y) * L * ldx + c;
+    // sums about the first value of the thread: exact enough unless that value lies many
+    // deviations off, and then it dominates the deviation itself
+    float pivot = 0.f, s = 0.f, ss = 0.f;
+    long cnt = 0;
+    if (member && l0 + prow < l1) {
+        float v[VEC];
+        load_vec<VEC>(v, base + (l0 + prow) * ldx);
+        pivot = v[0];
+#pragma unroll 4
+        for (long l = l0 + prow; l < l1; l += par) {
+            load_vec<VEC>(v, base + l * ldx);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float d = v[e] - pivot;
+                s += d;
+                ss = fmaf(d, d, ss);
+            }
+            cnt += VEC;
+        }
+    }
+    const float n = static_cast<float>(cnt);
+    Moments mine{n, 0.f, 0.f};
+    if (cnt) {
+        const float md = s / n;
+        mine.mean = pivot + md;
+        mine.m2 = fmaxf(ss - s * md, 0.f);
+    }
+    mom[threadIdx.x] = mine;
+    __syncthreads();
+    // one warp per group of the tile: its members' moments, lane by lane, then across lanes
+    const int cend = min(c0 + lanes * VEC, C);
+    const int warp = threadIdx.x / 32, ln = threadIdx.x % 32;
+    const long slot = (static_cast<long>(blockIdx.y) * gridDim.x + blockIdx.x) * gridDim.z + blockIdx.z;
+    const int G = C / Cg;
+    for (int g = c0 / Cg + warp; g * Cg < cend; g += kThreads / 32) {
+        const int a = (max(g * Cg, c0) - c0) / VEC, b = (min((g + 1) * Cg, cend) - c0) / VEC;
+        const int m = (b - a) * par;
+        Moments t{0.f, 0.f, 0.f};
+        for (int i = ln; i < m; i += 32) t = merge(t, mom[(i / (b - a)) * lanes + a + i % (b - a)]);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+            const Moments o{__shfl_down_sync(kFull, t.n, d), __shfl_down_sync(kFull, t.mean, d),
+                            __shfl_down_sync(kFull, t.m2, d)};
+            t = merge(t, o);
+        }
+        if (ln == 0) {
+            float* p = part + (slot * G + g) * 3;
+            p[0] = t.n, p[1] = t.mean, p[2] = t.m2;
+        }
+    }
+}
+
+// mean and rstd of every (sample, group) from the moments of its splits and tiles.
+__global__ void __launch_bounds__(kThreads)
+    norm_join_kernel(const float* __restrict__ part, float* __restrict__ stats, long units, int G, int Cg, int splits,
+                     int tiles, int tile_c, float eps) {
+    const long u = static_cast<long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+    const int ln = threadIdx.x % 32;
+    if (u >= units) return;
+    const long n = u / G;
+    const int g = static_cast<int>(u % G);
+    const int z0 = g * Cg / tile_c, z1 = ((g + 1) * Cg - 1) / tile_c;  // the tiles that hold the group
+    const int nz = z1 - z0 + 1;
+    Moments t{0.f, 0.f, 0.f};
+    for (int i = ln; i < splits * nz; i += 32) {
+        const long slot = (n * splits + i / nz) * tiles + z0 + i % nz;
+        const float* p = part + (slot * G + g) * 3;
+        t = merge(t, Moments{p[0], p[1], p[2]});
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+        const Moments o{__shfl_down_sync(kFull, t.n, d), __shfl_down_sync(kFull, t.mean, d),
+                        __shfl_down_sync(kFull, t.m2, d)};
+        t = merge(t, o);
+    }
+    if (ln == 0) {
+        stats[2 * u] = t.mean;
+        stats[2 * u + 1] = rstd_of(t.m2 / t.n, eps);
+    }
+}
+
+// y from x and the statistics; thread: one vector of channels, rows prow, prow + par, ..
+// of the split.  Groups of a vector's elements may differ, so each takes its own.
+template <typename IO, int VEC>
+__global__ void __launch_bounds__(kThreads)
+    norm_apply_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
+                      const float* __restrict__ bias, const float* __restrict__ stats, IO* __restrict__ y, long ldy,
+                      long L, int C, int Cg, int lanes, long split_rows, int act) {
+    const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
+    const int c = (blockIdx.z * lanes + lane) * VEC;
+    if (prow >= par || c >= C) return;
+    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
+    const long n = blockIdx.y;
+    const int g = c / Cg;  // VEC divides Cg or is 1
+    const float mean = stats[2 * (n * (C / Cg) + g)], rstd = stats[2 * (n * (C / Cg) + g) + 1];
+    float wv[VEC], bv[VEC];
+    load_param<VEC>(wv, weight, c, 1.f);
+    load_param<VEC>(bv, bias, c, 0.f);
+    const IO* src = x + n * L * ldx + c;
+    IO* dst = y + n * L * ldy + c;
+#pragma unroll 4
+    for (long l = l0 + prow; l < l1; l += par) {
+        float v[VEC];
+        load_vec<VEC>(v, src + l * ldx);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = act_f32(fmaf((v[e] - mean) * rstd, wv[e], bv[e]), act);
+        store_vec<VEC>(dst + l * ldy, v);
+    }
+}
+
+// Per (sample, split, channel): sum of q h and sum of q, part [sample][split][2][C].
+template <typename IO, int VEC>
+__global__ void __launch_bounds__(kThreads)
+    norm_bwd_sums_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
+                         const float* __restrict__ bias, const float* __restrict__ stats, const IO* __restrict__ dy,
+                         long lddy, float* __restrict__ part, long L, int C, int Cg, int lanes, long split_rows,
+                         int act) {
+    __shared__ float sums[2][kThreads * VEC];
+    const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
+    const int c = (blockIdx.z * lanes + lane) * VEC;
+    const bool member = prow < par && c < C;
+    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
+    const long n = blockIdx.y;
+    float aw[VEC], ab[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) aw[e] = ab[e] = 0.f;
+    if (member) {
+        const int g = c / Cg;
+        const float mean = stats[2 * (n * (C / Cg) + g)], rstd = stats[2 * (n * (C / Cg) + g) + 1];
+        float wv[VEC], bv[VEC];
+        load_param<VEC>(wv, weight, c, 1.f);
+        load_param<VEC>(bv, bias, c, 0.f);
+#pragma unroll 4
+        for (long l = l0 + prow; l < l1; l += par) {
+            float h[VEC], q[VEC];
+            load_vec<VEC>(h, x + (n * L + l) * ldx + c);
+            load_vec<VEC>(q, dy + (n * L + l) * lddy + c);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                h[e] = (h[e] - mean) * rstd;
+                q[e] *= act_grad_f32(fmaf(h[e], wv[e], bv[e]), act);
+                ab[e] += q[e];
+                aw[e] = fmaf(q[e], h[e], aw[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        sums[0][threadIdx.x * VEC + e] = aw[e];
+        sums[1][threadIdx.x * VEC + e] = ab[e];
+    }
+    __syncthreads();
+    if (prow != 0 || !member) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float s[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[e] = 0.f;
+        for (int t = 0; t < par; ++t)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[e] += sums[which][(t * lanes + lane) * VEC + e];
+        store_vec<VEC>(part + ((n * gridDim.x + blockIdx.x) * 2 + which) * C + c, s);
+    }
+}
+
+// m1 and m2 of every (sample, group): mom [units][2], one block each.
+__global__ void __launch_bounds__(kThreads)
+    norm_bwd_join_kernel(const float* __restrict__ part, const float* __restrict__ weight, float* __restrict__ mom,
+                         long L, int G, int Cg, int splits) {
+    __shared__ float red[kThreads / 32];
+    const long u = blockIdx.x, n = u / G, C = static_cast<long>(G) * Cg;
+    const int g = static_cast<int>(u % G);
+    float s1 = 0.f, s2 = 0.f;
+    for (long i = threadIdx.x; i < static_cast<long>(splits) * Cg; i += kThreads) {
+        const long sp = i / Cg, c = static_cast<long>(g) * Cg + i % Cg;
+        const float w = weight ? weight[c] : 1.f;
+        const float* p = part + (n * splits + sp) * 2 * C + c;
+        s2 = fmaf(w, p[0], s2);
+        s1 = fmaf(w, p[C], s1);
+    }
+    s1 = team_sum<kThreads>(s1, red);
+    s2 = team_sum<kThreads>(s2, red);
+    if (threadIdx.x == 0) {
+        const float cnt = static_cast<float>(L) * Cg;
+        mom[2 * u] = s1 / cnt;
+        mom[2 * u + 1] = s2 / cnt;
+    }
+}
+
+template <typename IO, int VEC>
+__global__ void __launch_bounds__(kThreads)
+    norm_bwd_apply_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
+                          const float* __restrict__ bias, const float* __restrict__ stats,
+                          const float* __restrict__ mom, const IO* __restrict__ dy, long lddy, IO* __restrict__ dx,
+                          long lddx, long L, int C, int Cg, int lanes, long split_rows, int act) {
+    const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
+    const int c = (blockIdx.z * lanes + lane) * VEC;
+    if (prow >= par || c >= C) return;
+    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
+    const long n = blockIdx.y, u = n * (C / Cg) + c / Cg;
+    const float mean = stats[2 * u], rstd = stats[2 * u + 1], m1 = mom[2 * u], m2 = mom[2 * u + 1];
+    float wv[VEC], bv[VEC];
+    load_param<VEC>(wv, weight, c, 1.f);
+    load_param<VEC>(bv, bias, c, 0.f);
+#pragma unroll 4
+    for (long l = l0 + prow; l < l1; l += par) {
+        float h[VEC], q[VEC];
+        load_vec<VEC>(h, x + (n * L + l) * ldx + c);
+        load_vec<VEC>(q, dy + (n * L + l) * lddy + c);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            h[e] = (h[e] - mean) * rstd;
+            q[e] *= act_grad_f32(fmaf(h[e], wv[e], bv[e]), act) * wv[e];
+            q[e] = rstd * (q[e] - m1 - h[e] * m2);
+        }
+        store_vec<VEC>(dx + (n * L + l) * lddx + c, q);
+    }
+}
+
+// ---------------------------------------------------------------- shapes
+// VEC elements per access: a 16-byte vector where groups and row strides allow it.
+template <typename IO>
+bool vec_ok(int Cg, long a, long b, long c) {
+    constexpr int v = kVec<IO>;
+    return Cg % v == 0 && a % v == 0 && b % v == 0 && c % v == 0;
+}
+
+// How the split form cuts [N][L][C]: `lanes` vectors of channels per tile, and splits
+// of the rows.  The partials' number is bounded by 8 per SM or one per 16 rows.
+struct Split {
+    int lanes, tiles, splits;
+    long split_rows;
+};
+Split split_of(long N, long L, int C, int vec) {
+    Split s;
+    const int nv = C / vec;
+    s.lanes = nv < kThreads ? nv : kThreads;
+    s.tiles = (nv + s.lanes - 1) / s.lanes;
+    const int par = kThreads / s.lanes;
+    const long want = (148L * 8 + N * s.tiles - 1) / (N * s.tiles);
+    const long most = (L + 16L * par - 1) / (16L * par);
+    const long n = want < most ? want : most;
+    s.split_rows = (L + n - 1) / n;
+    s.splits = static_cast<int>((L + s.split_rows - 1) / s.split_rows);
+    return s;
+}
+
+// The row form's team: the smallest that holds nv vectors, 0 when none does.
+// Up to 32 lanes hold one vector each, one warp 2 or 4, a block 1 to 4.
+int team_of(int nv) {
+    for (int t = 1; t <= 32; t <<= 1)
+        if (nv <= t) return t;
+    if (nv <= 64) return 64;     // 32 lanes x 2
+    if (nv <= 128) return 128;   // 32 lanes x 4
+    if (nv <= 256) return 256;   // 256 threads x 1
+    if (nv <= 1024) return 1024;  // 256 threads x 4
+    return 0;
+}
+int team_threads(int team) { return team <= 32 ? team : team <= 128 ? 32 : 256; }
+
+// Blocks of rows in the row form's backward: two blocks per SM share the column of
+// groups, each with at least one turn.
+struct RowBwd {
+    int gpb, gx;
+    long gy;
+};
+RowBwd row_bwd_of(long N, int G, int team) {
+    RowBwd r;
+    const int teams = kThreads / team_threads(team);
+    r.gpb = G < teams ? G : teams;
+    r.gx = (G + r.gpb - 1) / r.gpb;
+    const int rpb = teams / r.gpb;
+    long gy = (148L * 4 + r.gx - 1) / r.gx;
+    const long most = (N + rpb - 1) / rpb;
+    r.gy = gy < most ? gy : most;
+    return r;
+}
+
+#define WKV7_NORM_TEAMS(CALL)              \
+    switch (team) {                        \
+        case 1: CALL(1, 1); break;         \
+        case 2: CALL(2, 1); break;         \
+        case 4: CALL(4, 1); break;         \
+        case 8: CALL(8, 1); break;         \
+        case 16: CALL(16, 1); break;       \
+        case 32: CALL(32, 1); break;       \
+        case 64: CALL(32, 2); break;       \
+        case 128: CALL(32, 4); break;      \
+        case 256: CALL(256, 1); break;     \
+        default: CALL(256, 4); break;      \
+    }
+
+template <typename IO, int VEC>
+cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
+    const int Cg = p.C / p.G;
+    const IO* x = static_cast<const IO*>(p.x);
+    IO* y = static_cast<IO*>(p.y);
+    const long units = static_cast<long>(p.N) * p.G;
+    const int team = p.L == 1 ? team_of(Cg / VEC) : 0;
+    if (team) {
+        const int per = kThreads / team_threads(team);
+        const unsigned blocks = static_cast<unsigned>((units + per - 1) / per);
+#define CALL(TEAM, K)                                                                                              \
+    norm_row_kernel<IO, VEC, TEAM, K><<<blocks, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, y, p.ldy, p.stats,  \
+                                                                   units, p.G, Cg, p.eps, p.act)
+        WKV7_NORM_TEAMS(CALL)
+#undef CALL
+        return cudaGetLastError();
+    }
+    const Split s = split_of(p.N, p.L, p.C, VEC);
+    float* part = p.ws;
+    float* stats = p.stats ? p.stats : part + static_cast<size_t>(p.N) * s.splits * s.tiles * p.G * 3;
+    const dim3 grid(s.splits, p.N, s.tiles);
+    norm_stats_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, part, p.L, p.C, Cg, s.lanes, s.split_rows);
+    norm_join_kernel<<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, st>>>(
+        part, stats, units, p.G, Cg, s.splits, s.tiles, s.lanes * VEC, p.eps);
+    norm_apply_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, stats, y, p.ldy, p.L, p.C, Cg,
+                                                          s.lanes, s.split_rows, p.act);
+    return cudaGetLastError();
+}
+
+template <typename IO, int VEC>
+cudaError_t norm_bwd_typed(const NormBwdArgs& p, cudaStream_t st) {
+    const int Cg = p.C / p.G;
+    const IO *x = static_cast<const IO*>(p.x), *dy = static_cast<const IO*>(p.dy);
+    IO* dx = static_cast<IO*>(p.dx);
+    const int team = p.L == 1 ? team_of(Cg / VEC) : 0;
+    long nblk;
+    if (p.N == 0 || p.L == 0) {
+        nblk = 0;  // no rows: dweight and dbias are zero
+    } else if (team) {
+        const RowBwd r = row_bwd_of(p.N, p.G, team);
+        const dim3 grid(r.gx, static_cast<unsigned>(r.gy));
+        nblk = r.gy;
+#define CALL(TEAM, K)                                                                                             \
+    norm_row_bwd_kernel<IO, VEC, TEAM, K><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, dy,     \
+                                                                     p.lddy, dx, p.lddx, p.ws, p.N, p.G, Cg,      \
+                                                                     r.gpb, p.act)
+        WKV7_NORM_TEAMS(CALL)
+#undef CALL
+    } else {
+        const Split s = split_of(p.N, p.L, p.C, VEC);
+        nblk = static_cast<long>(p.N) * s.splits;
+        float* mom = p.ws + static_cast<size_t>(nblk) * 2 * p.C;
+        const dim3 grid(s.splits, p.N, s.tiles);
+        norm_bwd_sums_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, dy, p.lddy,
+                                                                 p.ws, p.L, p.C, Cg, s.lanes, s.split_rows, p.act);
+        norm_bwd_join_kernel<<<static_cast<unsigned>(static_cast<long>(p.N) * p.G), kThreads, 0, st>>>(
+            p.ws, p.weight, mom, p.L, p.G, Cg, s.splits);
+        norm_bwd_apply_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, mom, dy,
+                                                                  p.lddy, dx, p.lddx, p.L, p.C, Cg, s.lanes,
+                                                                  s.split_rows, p.act);
+    }
+    if (p.dw || p.db)
+        norm_sum_kernel<<<static_cast<unsigned>((2L * p.C + 31) / 32), kThreads, 0, st>>>(p.ws, p.dw, p.db, nblk,
+                                                                                          p.C);
+    return cudaGetLastError();
+}
+
+// Workspace of either vector width (the width depends on the row strides, which the
+// size query does not know): the larger.
+template <typename IO>
+size_t ws_floats(int N, int L, int C, int G, bool backward) {
+    size_t most = 0;
+    const int Cg = C / G;
+    for (int vec : {1, kVec<IO>}) {
+        if (Cg % vec) continue;
+        const int team = L == 1 ? team_of(Cg / vec) : 0;
+        size_t n = 0;
+        if (team) {
+            if (backward) n = static_cast<size_t>(row_bwd_of(N, G, team).gy) * 2 * C;
+        } else {
+            const Split s = split_of(N, L, C, vec);
+            n = backward ? static_cast<size_t>(N) * s.splits * 2 * C + static_cast<size_t>(N) * G * 2
+                         : static_cast<size_t>(N) * s.splits * s.tiles * G * 3 + static_cast<size_t>(N) * G * 2;
+        }
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
+}  // namespace
+
+size_t norm_workspace_floats(int N, int L, int C, int G, int io_dtype, bool backward) {
+    if (N == 0 || L == 0) return 0;
+    return io_dtype == WKV7_BF16 ? ws_floats<__nv_bfloat16>(N, L, C, G, backward)
+                                 : ws_floats<float>(N, L, C, G, backward);
+}
+
+cudaError_t launch_norm(const NormArgs& p, int io_dtype, cudaStream_t stream) {
+    const int Cg = p.C / p.G;
+    if (io_dtype == WKV7_BF16)
+        return vec_ok<__nv_bfloat16>(Cg, p.ldx, p.ldy, 0) ? norm_typed<__nv_bfloat16, 8>(p, stream)
+                                                          : norm_typed<__nv_bfloat16, 1>(p, stream);
+    return vec_ok<float>(Cg, p.ldx, p.ldy, 0) ? norm_typed<float, 4>(p, stream) : norm_typed<float, 1>(p, stream);
+}
+
+cudaError_t launch_norm_backward(const NormBwdArgs& p, int io_dtype, cudaStream_t stream) {
+    const int Cg = p.C / p.G;
+    if (io_dtype == WKV7_BF16)
+        return vec_ok<__nv_bfloat16>(Cg, p.ldx, p.lddy, p.lddx) ? norm_bwd_typed<__nv_bfloat16, 8>(p, stream)
+                                                                : norm_bwd_typed<__nv_bfloat16, 1>(p, stream);
+    return vec_ok<float>(Cg, p.ldx, p.lddy, p.lddx) ? norm_bwd_typed<float, 4>(p, stream)
+                                                    : norm_bwd_typed<float, 1>(p, stream);
+}
+
+}  // namespace wkv7
