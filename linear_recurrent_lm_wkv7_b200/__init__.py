@@ -11,6 +11,8 @@ kernels.
 """
 from __future__ import annotations
 
+import functools
+
 from ._binding import (  # noqa: F401
     EXPORTS,
     LIB_PATH,
@@ -260,16 +262,27 @@ def decode_step(r, w_log, k, v, a, b, state, y=None, stream=None):
 
 
 # ---------------------------------------------------------------- state-space layers
+class _NoStream:
+    """The current stream stays the current one."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_NO_STREAM = _NoStream()
+
+
 def _outputs(like, stream, inputs):
     """The context in which outputs and workspaces of a call on ``stream`` are allocated:
     that stream's, so that the allocator hands their memory on only in its order.  The
     inputs are marked as used there."""
-    import contextlib
-
+    if stream is None:
+        return _NO_STREAM
     import torch
 
-    if stream is None:
-        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), like.device)
     for t in inputs:
@@ -278,17 +291,20 @@ def _outputs(like, stream, inputs):
     return torch.cuda.stream(stream)
 
 
-def _scratch(nbytes, device):
-    import torch
+@functools.lru_cache(maxsize=256)
+def _bytes(query, *sizes):
+    """A workspace's size, asked of the library once per problem size."""
+    return query(*sizes)
 
-    return torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device) if nbytes else None
+
+def _scratch(nbytes, like):
+    """A workspace of at least ``nbytes`` bytes on the device of ``like``, or none."""
+    return like.new_empty((nbytes + like.element_size() - 1) // like.element_size()) if nbytes else None
 
 
-def _new(t, dtype=None):
-    """A contiguous tensor of the shape and device of ``t``."""
-    import torch
-
-    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
+def _new(t):
+    """A contiguous tensor of the shape, type and device of ``t``."""
+    return t.new_empty(t.shape)
 
 
 def _rows(t, seq_offsets, inner):
@@ -336,8 +352,7 @@ def causal_conv_backward(x, w, dy, bias=None, s0=None, dsT=None, seq_offsets=Non
     C, W = w.shape
     with _outputs(x, stream, (x, w, dy, bias, s0, dsT, seq_offsets, workspace)):
         if workspace is None:
-            workspace = _scratch(wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, seq_offsets is not None),
-                                 x.device)
+            workspace = _scratch(_bytes(wkv7_causal_conv_backward_workspace_bytes, B, T, C, W, seq_offsets is not None), x)
         dx, dw = _new(x), _new(w)
         dbias = _new(bias) if bias is not None else None
         ds0 = x.new_empty((B, W - 1, C))
@@ -360,8 +375,7 @@ def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, s0=None, seq_offsets=
     G, N = Bm.shape[-2:]
     with _outputs(x, stream, (x, dt, A, Bm, Cm, D, dt_bias, s0, seq_offsets, workspace)):
         if workspace is None:
-            workspace = _scratch(wkv7_selective_scan_workspace_bytes(B, T, H, P, N, seq_offsets is not None),
-                                 x.device)
+            workspace = _scratch(_bytes(wkv7_selective_scan_workspace_bytes, B, T, H, P, N, seq_offsets is not None), x)
         y = _new(x)
         sT = A.new_empty((B, H, P, N)) if want_state else None
     wkv7_selective_scan(x, dt, A, Bm, Cm, D, dt_bias, s0, y, sT, workspace, B, T, H, P, N, G, seq_offsets,
@@ -394,8 +408,7 @@ def selective_scan_backward(x, dt, A, Bm, Cm, dy, D=None, dt_bias=None, s0=None,
     with _outputs(x, stream, (x, dt, A, Bm, Cm, dy, D, dt_bias, s0, dsT, seq_offsets, workspace)):
         if workspace is None:
             workspace = _scratch(
-                wkv7_selective_scan_backward_workspace_bytes(B, T, H, P, N, G, _code(x), seq_offsets is not None),
-                x.device)
+                _bytes(wkv7_selective_scan_backward_workspace_bytes, B, T, H, P, N, G, _code(x), seq_offsets is not None), x)
         dx, ddt, dA, dB, dC = (_new(t) for t in (x, dt, A, Bm, Cm))
         dD = _new(D) if D is not None else None
         dbias = _new(dt_bias) if dt_bias is not None else None
@@ -414,7 +427,7 @@ def group_norm(x, groups, weight=None, bias=None, eps=1e-5, act=None, want_stats
     N, L, C = x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[-1])
     with _outputs(x, stream, (x, weight, bias, workspace)):
         if workspace is None:
-            workspace = _scratch(wkv7_group_norm_workspace_bytes(N, L, C, groups, _code(x)), x.device)
+            workspace = _scratch(_bytes(wkv7_group_norm_workspace_bytes, N, L, C, groups, _code(x)), x)
         y = _new(x)
         stats = _float32(x, (N, groups, 2)) if want_stats else None
     wkv7_group_norm(x, weight, bias, y, stats, workspace, N, L, C, groups, eps, act, stream)
@@ -427,7 +440,7 @@ def group_norm_backward(x, groups, stats, dy, weight=None, bias=None, act=None, 
     N, L, C = x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[-1])
     with _outputs(x, stream, (x, stats, dy, weight, bias, workspace)):
         if workspace is None:
-            workspace = _scratch(wkv7_group_norm_backward_workspace_bytes(N, L, C, groups, _code(x)), x.device)
+            workspace = _scratch(_bytes(wkv7_group_norm_backward_workspace_bytes, N, L, C, groups, _code(x)), x)
         dx = _new(x)
         dw = _new(weight) if weight is not None else None
         db = _new(bias) if bias is not None else None

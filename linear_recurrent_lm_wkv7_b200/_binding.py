@@ -281,7 +281,34 @@ def wkv7_decode_step(r, w_log, k, v, a, b, s_in, y, s_out, B, H, D, stream=None)
 
 
 # ---- causal convolution, selective scan, group norm: rows at a stride
+#
+# These calls check types, shapes, strides and devices of every tensor.  A single token
+# per sequence takes the GPU a few microseconds, so the checks are written to be quick:
+# one function call per tensor, and none of torch's slower queries.
 WKV7_ACT = {None: 0, "none": 0, "silu": 1}
+
+
+class _Runtime:
+    """What the calls use of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+
+        self.f32, self.i32 = torch.float32, torch.int32
+        self.codes = {torch.float32: WKV7_F32, torch.bfloat16: WKV7_BF16}
+        self.device = torch.cuda.device
+        self.current_device = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_RT = None
+
+
+def _runtime():
+    global _RT
+    if _RT is None:
+        _RT = _Runtime()
+    return _RT
 
 
 def _act(act):
@@ -292,22 +319,19 @@ def _act(act):
 
 
 def _code(t):
-    import torch
-
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return WKV7_BF16
-    if dt is torch.float32:
-        return WKV7_F32
-    raise TypeError(f"unsupported dtype {dt}")
+    c = _runtime().codes.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return c
 
 
 def _row_ld(t, lead, width, name):
     """The row stride, in elements, of a tensor whose first ``lead`` dimensions number
     rows of ``width`` elements; the other dimensions have to be contiguous."""
+    if t.is_contiguous():
+        # of one row or none any stride that covers it will do
+        return width if t.numel() > width else -(-width // 8) * 8
     shape, stride = t.shape, t.stride()
-    if 0 in shape:  # no rows: any stride that covers one will do
-        return -(-width // 8) * 8
     inner = 1
     for k in range(len(shape) - 1, lead - 1, -1):
         if shape[k] != 1 and stride[k] != inner:
@@ -325,109 +349,89 @@ def _row_ld(t, lead, width, name):
     return ld if rows > 1 else -(-width // 8) * 8
 
 
-def _at(device, **tensors):
-    """The raw pointers of tensors that may be None, all on one device."""
-    out = []
-    for name, t in tensors.items():
-        if t is None:
-            out.append(None)
-            continue
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        out.append(t.data_ptr())
-    return out
-
-
-def _need(t, name, dtype, shape):
-    """An optional contiguous tensor of a given type and shape."""
-    if t is None:
-        return
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _cuda(t):
+def _wrong(t, name, dtype, shape, dev):
+    """Raises what is wrong with a tensor that did not pass a check."""
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    return t.device
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _call(device, stream, fn, args, where):
-    """Calls the library with ``device`` current and raises on a status."""
-    import torch
+def _flat(t, name, dtype, shape, dev):
+    """The pointer of a contiguous tensor of a given type and shape, or of none."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _wrong(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
+
+def _rows(t, name, dtype, shape, lead, width, dev):
+    """The pointer and the row stride of rows of ``width`` elements."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _wrong(t, name, dtype, shape, dev)
+    return t.data_ptr(), _row_ld(t, lead, width, name)
+
+
+def _space(t, dev):
+    """The pointer and the bytes of a workspace, or of none."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _wrong(t, "workspace", t.dtype, t.shape, dev)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _dev(t):
+    """The ordinal of the device that a call runs on."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    return t.get_device()
+
+
+def _call(dev, stream, fn, args, where):
+    """Calls the library with device ``dev`` current and raises on a status."""
+    rt = _runtime()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, handle)
+        stream = rt.raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if rt.current_device() == dev:
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
+        with rt.device(dev):
+            st = fn(*args, stream)
     if st != 0:
         raise Wkv7Error(st, where)
-
-
-def _packed(seq_offsets, B):
-    import torch
-
-    _need(seq_offsets, "seq_offsets", torch.int32, (B + 1,))
-
-
-def _like(t, ref, name):
-    if t.dtype is not ref.dtype:
-        raise TypeError(f"{name} must be {ref.dtype}, not {t.dtype}")
-    if t.shape != ref.shape:
-        raise ValueError(f"{name} must have the shape {tuple(ref.shape)}, not {tuple(t.shape)}")
-
-
-def _leading(t, inner, B, T, seq_offsets, name):
-    """How many dimensions number rows ([B, T, ..] or packed [T, ..]), after a check."""
-    lead = (T,) if seq_offsets is not None else (B, T)
-    if tuple(t.shape) != lead + tuple(inner):
-        raise ValueError(f"{name} must have the shape {lead + tuple(inner)}, not {tuple(t.shape)}")
-    return len(lead)
 
 
 def wkv7_causal_conv(x, w, bias, s0, y, sT, B, T, C, W, seq_offsets=None, act=None, stream=None):
     """Enqueue the causal convolution (see include/wkv7.h).  x and y may be slices of
     wider rows."""
-    import torch
-
-    dev = _cuda(x)
-    lead = _leading(x, (C,), B, T, seq_offsets, "x")
-    _like(y, x, "y")
-    _need(w, "w", torch.float32, (C, W))
-    _need(bias, "bias", torch.float32, (C,))
-    _need(s0, "s0", x.dtype, (B, W - 1, C))
-    _need(sT, "sT", x.dtype, (B, W - 1, C))
-    _packed(seq_offsets, B)
-    px, pw, pb, p0, py, pT, po = _at(dev, x=x, w=w, bias=bias, s0=s0, y=y, sT=sT, seq_offsets=seq_offsets)
+    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    lead = (B, T) if seq_offsets is None else (T,)
+    px, ldx = _rows(x, "x", io, lead + (C,), len(lead), C, dev)
+    py, ldy = _rows(y, "y", io, lead + (C,), len(lead), C, dev)
     _call(dev, stream, _lib().wkv7_causal_conv,
-          (px, _row_ld(x, lead, C, "x"), pw, pb, p0, py, _row_ld(y, lead, C, "y"), pT, B, T, C, W, po, _act(act),
-           _code(x)), "wkv7_causal_conv")
+          (px, ldx, _flat(w, "w", f32, (C, W), dev), _flat(bias, "bias", f32, (C,), dev),
+           _flat(s0, "s0", io, (B, W - 1, C), dev), py, ldy, _flat(sT, "sT", io, (B, W - 1, C), dev), B, T, C, W,
+           _flat(seq_offsets, "seq_offsets", _RT.i32, (B + 1,), dev), _act(act), code), "wkv7_causal_conv")
 
 
 def wkv7_causal_conv_step(x, w, bias, s_in, y, s_out, B, C, W, act=None, stream=None):
     """Enqueue one token per sequence of the causal convolution (see include/wkv7.h)."""
-    import torch
-
-    dev = _cuda(x)
-    if tuple(x.shape) != (B, C):
-        raise ValueError(f"x must have the shape {(B, C)}, not {tuple(x.shape)}")
-    _like(y, x, "y")
-    _need(w, "w", torch.float32, (C, W))
-    _need(bias, "bias", torch.float32, (C,))
-    _need(s_in, "s_in", x.dtype, (B, W - 1, C))
-    _need(s_out, "s_out", x.dtype, (B, W - 1, C))
-    px, pw, pb, p0, py, pT = _at(dev, x=x, w=w, bias=bias, s_in=s_in, y=y, s_out=s_out)
+    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    px, ldx = _rows(x, "x", io, (B, C), 1, C, dev)
+    py, ldy = _rows(y, "y", io, (B, C), 1, C, dev)
     _call(dev, stream, _lib().wkv7_causal_conv_step,
-          (px, _row_ld(x, 1, C, "x"), pw, pb, p0, py, _row_ld(y, 1, C, "y"), pT, B, C, W, _act(act), _code(x)),
-          "wkv7_causal_conv_step")
+          (px, ldx, _flat(w, "w", f32, (C, W), dev), _flat(bias, "bias", f32, (C,), dev),
+           _flat(s_in, "s_in", io, (B, W - 1, C), dev), py, ldy, _flat(s_out, "s_out", io, (B, W - 1, C), dev), B, C,
+           W, _act(act), code), "wkv7_causal_conv_step")
 
 
 def wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, packed) -> int:
@@ -437,48 +441,30 @@ def wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, packed) -> int:
 def wkv7_causal_conv_backward(x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, workspace, B, T, C, W, seq_offsets=None,
                               act=None, stream=None):
     """Enqueue the gradient of the causal convolution (see include/wkv7.h)."""
-    import torch
-
-    dev = _cuda(x)
-    lead = _leading(x, (C,), B, T, seq_offsets, "x")
-    _like(dy, x, "dy")
-    _like(dx, x, "dx")
-    for t, name in ((w, "w"), (dw, "dw")):
-        _need(t, name, torch.float32, (C, W))
-    for t, name in ((bias, "bias"), (dbias, "dbias")):
-        _need(t, name, torch.float32, (C,))
-    for t, name in ((s0, "s0"), (dsT, "dsT"), (ds0, "ds0")):
-        _need(t, name, x.dtype, (B, W - 1, C))
-    _packed(seq_offsets, B)
-    px, pw, pb, p0, pdy, pdT, pdx, pdw, pdb, pd0, ws, po = _at(
-        dev, x=x, w=w, bias=bias, s0=s0, dy=dy, dsT=dsT, dx=dx, dw=dw, dbias=dbias, ds0=ds0, workspace=workspace,
-        seq_offsets=seq_offsets)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    lead = (B, T) if seq_offsets is None else (T,)
+    k, shape, st = len(lead), lead + (C,), (B, W - 1, C)
+    px, ldx = _rows(x, "x", io, shape, k, C, dev)
+    pdy, lddy = _rows(dy, "dy", io, shape, k, C, dev)
+    pdx, lddx = _rows(dx, "dx", io, shape, k, C, dev)
+    ws, nbytes = _space(workspace, dev)
     _call(dev, stream, _lib().wkv7_causal_conv_backward,
-          (px, _row_ld(x, lead, C, "x"), pw, pb, p0, pdy, _row_ld(dy, lead, C, "dy"), pdT, pdx,
-           _row_ld(dx, lead, C, "dx"), pdw, pdb, pd0, ws, nbytes, B, T, C, W, po, _act(act), _code(x)),
+          (px, ldx, _flat(w, "w", f32, (C, W), dev), _flat(bias, "bias", f32, (C,), dev),
+           _flat(s0, "s0", io, st, dev), pdy, lddy, _flat(dsT, "dsT", io, st, dev), pdx, lddx,
+           _flat(dw, "dw", f32, (C, W), dev), _flat(dbias, "dbias", f32, (C,), dev), _flat(ds0, "ds0", io, st, dev),
+           ws, nbytes, B, T, C, W, _flat(seq_offsets, "seq_offsets", _RT.i32, (B + 1,), dev), _act(act), code),
           "wkv7_causal_conv_backward")
 
 
-def _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, B, T, H, D, N, G, seq_offsets, step):
-    import torch
-
-    if step:
-        seq_offsets, lead = None, 1
-        for t, inner, name in ((x, (H, D), "x"), (dt, (H,), "dt"), (Bm, (G, N), "Bm"), (Cm, (G, N), "Cm")):
-            if tuple(t.shape) != (B,) + inner:
-                raise ValueError(f"{name} must have the shape {(B,) + inner}, not {tuple(t.shape)}")
-    else:
-        lead = _leading(x, (H, D), B, T, seq_offsets, "x")
-        _leading(dt, (H,), B, T, seq_offsets, "dt")
-        _leading(Bm, (G, N), B, T, seq_offsets, "Bm")
-        _leading(Cm, (G, N), B, T, seq_offsets, "Cm")
-    if Bm.dtype is not x.dtype or Cm.dtype is not x.dtype:
-        raise TypeError(f"Bm and Cm must be {x.dtype}, as x is")
-    for t, name in ((A, "A"), (D_skip, "D_skip"), (dt_bias, "dt_bias")):
-        _need(t, name, torch.float32, (H,))
-    return (lead, _row_ld(x, lead, H * D, "x"), _row_ld(dt, lead, H, "dt"), _row_ld(Bm, lead, G * N, "Bm"),
-            _row_ld(Cm, lead, G * N, "Cm"))
+def _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, lead, H, D, N, G, dev):
+    """The leading arguments that the scan's calls share: x to dt_bias."""
+    f32, io, k = _RT.f32, x.dtype, len(lead)
+    px, ldx = _rows(x, "x", io, lead + (H, D), k, H * D, dev)
+    pt, ldt = _rows(dt, "dt", dt.dtype, lead + (H,), k, H, dev)
+    pb, ldb = _rows(Bm, "Bm", io, lead + (G, N), k, G * N, dev)
+    pc, ldc = _rows(Cm, "Cm", io, lead + (G, N), k, G * N, dev)
+    return (px, ldx, pt, ldt, _flat(A, "A", f32, (H,), dev), pb, ldb, pc, ldc,
+            _flat(D_skip, "D_skip", f32, (H,), dev), _flat(dt_bias, "dt_bias", f32, (H,), dev))
 
 
 def wkv7_selective_scan_workspace_bytes(B, T, H, D, N, packed) -> int:
@@ -489,38 +475,27 @@ def wkv7_selective_scan(x, dt, A, Bm, Cm, D_skip, dt_bias, s0, y, sT, workspace,
                         dt_softplus=True, stream=None):
     """Enqueue the selective scan (see include/wkv7.h).  x, dt, Bm, Cm and y may be
     slices of wider rows."""
-    import torch
-
-    dev = _cuda(x)
-    lead, ldx, lddt, ldb, ldc = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, B, T, H, D, N, G, seq_offsets, False)
-    _like(y, x, "y")
-    _need(s0, "s0", torch.float32, (B, H, D, N))
-    _need(sT, "sT", torch.float32, (B, H, D, N))
-    _packed(seq_offsets, B)
-    px, pdt, pA, pB, pC, pD, pb, p0, py, pT, ws, po = _at(
-        dev, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D_skip=D_skip, dt_bias=dt_bias, s0=s0, y=y, sT=sT, workspace=workspace,
-        seq_offsets=seq_offsets)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    f32, dev, code, dtc = _runtime().f32, _dev(x), _code(x), _code(dt)
+    lead = (B, T) if seq_offsets is None else (T,)
+    ins = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, lead, H, D, N, G, dev)
+    ws, nbytes = _space(workspace, dev)
     _call(dev, stream, _lib().wkv7_selective_scan,
-          (px, ldx, pdt, lddt, pA, pB, ldb, pC, ldc, pD, pb, p0, py, _row_ld(y, lead, H * D, "y"), pT, ws, nbytes, B,
-           T, H, D, N, G, po, 1 if dt_softplus else 0, _code(x), _code(dt)), "wkv7_selective_scan")
+          ins + (_flat(s0, "s0", f32, (B, H, D, N), dev),) +
+          _rows(y, "y", x.dtype, lead + (H, D), len(lead), H * D, dev) +
+          (_flat(sT, "sT", f32, (B, H, D, N), dev), ws, nbytes, B, T, H, D, N, G,
+           _flat(seq_offsets, "seq_offsets", _RT.i32, (B + 1,), dev), 1 if dt_softplus else 0, code, dtc),
+          "wkv7_selective_scan")
 
 
 def wkv7_selective_scan_step(x, dt, A, Bm, Cm, D_skip, dt_bias, s_in, y, s_out, B, H, D, N, G, dt_softplus=True,
                              stream=None):
     """Enqueue one token per sequence of the selective scan (see include/wkv7.h)."""
-    import torch
-
-    dev = _cuda(x)
-    _, ldx, lddt, ldb, ldc = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, B, 1, H, D, N, G, None, True)
-    _like(y, x, "y")
-    _need(s_in, "s_in", torch.float32, (B, H, D, N))
-    _need(s_out, "s_out", torch.float32, (B, H, D, N))
-    px, pdt, pA, pB, pC, pD, pb, p0, py, pT = _at(dev, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D_skip=D_skip, dt_bias=dt_bias,
-                                                  s_in=s_in, y=y, s_out=s_out)
+    f32, dev, code, dtc = _runtime().f32, _dev(x), _code(x), _code(dt)
     _call(dev, stream, _lib().wkv7_selective_scan_step,
-          (px, ldx, pdt, lddt, pA, pB, ldb, pC, ldc, pD, pb, p0, py, _row_ld(y, 1, H * D, "y"), pT, B, H, D, N, G,
-           1 if dt_softplus else 0, _code(x), _code(dt)), "wkv7_selective_scan_step")
+          _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, (B,), H, D, N, G, dev) +
+          (_flat(s_in, "s_in", f32, (B, H, D, N), dev),) + _rows(y, "y", x.dtype, (B, H, D), 1, H * D, dev) +
+          (_flat(s_out, "s_out", f32, (B, H, D, N), dev), B, H, D, N, G, 1 if dt_softplus else 0, code, dtc),
+          "wkv7_selective_scan_step")
 
 
 def wkv7_selective_scan_backward_workspace_bytes(B, T, H, D, N, G, io_dtype, packed) -> int:
@@ -531,34 +506,24 @@ def wkv7_selective_scan_backward(x, dt, A, Bm, Cm, D_skip, dt_bias, s0, dy, dsT,
                                  ds0, workspace, B, T, H, D, N, G, seq_offsets=None, dt_softplus=True, stream=None):
     """Enqueue the gradient of the selective scan (see include/wkv7.h).  dx, dB and dC may
     be column slices of one buffer, for the convolution's backward to take."""
-    import torch
-
-    dev = _cuda(x)
-    lead, ldx, lddt, ldb, ldc = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, B, T, H, D, N, G, seq_offsets, False)
-    for t, ref, name in ((dy, x, "dy"), (dx, x, "dx"), (ddt, dt, "ddt"), (dB, Bm, "dB"), (dC, Cm, "dC")):
-        _like(t, ref, name)
-    for t, name in ((dA, "dA"), (dD, "dD"), (ddt_bias, "ddt_bias")):
-        _need(t, name, torch.float32, (H,))
-    for t, name in ((s0, "s0"), (dsT, "dsT"), (ds0, "ds0")):
-        _need(t, name, torch.float32, (B, H, D, N))
-    _packed(seq_offsets, B)
-    px, pdt, pA, pB, pC, pD, pb, p0, pdy, pdT = _at(dev, x=x, dt=dt, A=A, Bm=Bm, Cm=Cm, D_skip=D_skip,
-                                                    dt_bias=dt_bias, s0=s0, dy=dy, dsT=dsT)
-    qx, qdt, qA, qB, qC, qD, qb, q0, ws, po = _at(dev, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, ddt_bias=ddt_bias,
-                                                  ds0=ds0, workspace=workspace, seq_offsets=seq_offsets)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    f32, dev, code, dtc = _runtime().f32, _dev(x), _code(x), _code(dt)
+    lead = (B, T) if seq_offsets is None else (T,)
+    k, io, st = len(lead), x.dtype, (B, H, D, N)
+    ins = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, lead, H, D, N, G, dev)
+    ws, nbytes = _space(workspace, dev)
     _call(dev, stream, _lib().wkv7_selective_scan_backward,
-          (px, ldx, pdt, lddt, pA, pB, ldb, pC, ldc, pD, pb, p0, pdy, _row_ld(dy, lead, H * D, "dy"), pdT, qx,
-           _row_ld(dx, lead, H * D, "dx"), qdt, _row_ld(ddt, lead, H, "ddt"), qA, qB,
-           _row_ld(dB, lead, G * N, "dB"), qC, _row_ld(dC, lead, G * N, "dC"), qD, qb, q0, ws, nbytes, B, T, H, D, N,
-           G, po, 1 if dt_softplus else 0, _code(x), _code(dt)), "wkv7_selective_scan_backward")
+          ins + (_flat(s0, "s0", f32, st, dev),) + _rows(dy, "dy", io, lead + (H, D), k, H * D, dev) +
+          (_flat(dsT, "dsT", f32, st, dev),) + _rows(dx, "dx", io, lead + (H, D), k, H * D, dev) +
+          _rows(ddt, "ddt", dt.dtype, lead + (H,), k, H, dev) + (_flat(dA, "dA", f32, (H,), dev),) +
+          _rows(dB, "dB", io, lead + (G, N), k, G * N, dev) + _rows(dC, "dC", io, lead + (G, N), k, G * N, dev) +
+          (_flat(dD, "dD", f32, (H,), dev), _flat(ddt_bias, "ddt_bias", f32, (H,), dev),
+           _flat(ds0, "ds0", f32, st, dev), ws, nbytes, B, T, H, D, N, G,
+           _flat(seq_offsets, "seq_offsets", _RT.i32, (B + 1,), dev), 1 if dt_softplus else 0, code, dtc),
+          "wkv7_selective_scan_backward")
 
 
-def _norm_dims(x, N, L, C, name="x"):
-    want = (N, C) if x.dim() == 2 and L == 1 else (N, L, C)
-    if tuple(x.shape) != want:
-        raise ValueError(f"{name} must have the shape {want}, not {tuple(x.shape)}")
-    return len(want) - 1
+def _norm_lead(x, N, L):
+    return (N,) if x.dim() == 2 and L == 1 else (N, L)
 
 
 def wkv7_group_norm_workspace_bytes(N, L, C, G, io_dtype) -> int:
@@ -567,19 +532,15 @@ def wkv7_group_norm_workspace_bytes(N, L, C, G, io_dtype) -> int:
 
 def wkv7_group_norm(x, weight, bias, y, stats, workspace, N, L, C, G, eps=1e-5, act=None, stream=None):
     """Enqueue the group norm (see include/wkv7.h)."""
-    import torch
-
-    dev = _cuda(x)
-    lead = _norm_dims(x, N, L, C)
-    _like(y, x, "y")
-    _need(weight, "weight", torch.float32, (C,))
-    _need(bias, "bias", torch.float32, (C,))
-    _need(stats, "stats", torch.float32, (N, G, 2))
-    px, pw, pb, py, ps, ws = _at(dev, x=x, weight=weight, bias=bias, y=y, stats=stats, workspace=workspace)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    lead = _norm_lead(x, N, L)
+    px, ldx = _rows(x, "x", io, lead + (C,), len(lead), C, dev)
+    py, ldy = _rows(y, "y", io, lead + (C,), len(lead), C, dev)
+    ws, nbytes = _space(workspace, dev)
     _call(dev, stream, _lib().wkv7_group_norm,
-          (px, _row_ld(x, lead, C, "x"), pw, pb, py, _row_ld(y, lead, C, "y"), ps, ws, nbytes, N, L, C, G, eps,
-           _act(act), _code(x)), "wkv7_group_norm")
+          (px, ldx, _flat(weight, "weight", f32, (C,), dev), _flat(bias, "bias", f32, (C,), dev), py, ldy,
+           _flat(stats, "stats", f32, (N, G, 2), dev), ws, nbytes, N, L, C, G, eps, _act(act), code),
+          "wkv7_group_norm")
 
 
 def wkv7_group_norm_backward_workspace_bytes(N, L, C, G, io_dtype) -> int:
@@ -589,22 +550,17 @@ def wkv7_group_norm_backward_workspace_bytes(N, L, C, G, io_dtype) -> int:
 def wkv7_group_norm_backward(x, weight, bias, stats, dy, dx, dweight, dbias, workspace, N, L, C, G, act=None,
                              stream=None):
     """Enqueue the gradient of the group norm (see include/wkv7.h)."""
-    import torch
-
-    dev = _cuda(x)
-    lead = _norm_dims(x, N, L, C)
-    _like(dy, x, "dy")
-    _like(dx, x, "dx")
-    for t, name in ((weight, "weight"), (bias, "bias"), (dweight, "dweight"), (dbias, "dbias")):
-        _need(t, name, torch.float32, (C,))
-    _need(stats, "stats", torch.float32, (N, G, 2))
-    px, pw, pb, ps, pdy, pdx, pdw, pdb, ws = _at(dev, x=x, weight=weight, bias=bias, stats=stats, dy=dy, dx=dx,
-                                                 dweight=dweight, dbias=dbias, workspace=workspace)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    lead = _norm_lead(x, N, L)
+    k, shape = len(lead), lead + (C,)
+    px, ldx = _rows(x, "x", io, shape, k, C, dev)
+    pdy, lddy = _rows(dy, "dy", io, shape, k, C, dev)
+    pdx, lddx = _rows(dx, "dx", io, shape, k, C, dev)
+    ws, nbytes = _space(workspace, dev)
     _call(dev, stream, _lib().wkv7_group_norm_backward,
-          (px, _row_ld(x, lead, C, "x"), pw, pb, ps, pdy, _row_ld(dy, lead, C, "dy"), pdx,
-           _row_ld(dx, lead, C, "dx"), pdw, pdb, ws, nbytes, N, L, C, G, _act(act), _code(x)),
-          "wkv7_group_norm_backward")
+          (px, ldx, _flat(weight, "weight", f32, (C,), dev), _flat(bias, "bias", f32, (C,), dev),
+           _flat(stats, "stats", f32, (N, G, 2), dev), pdy, lddy, pdx, lddx, _flat(dweight, "dweight", f32, (C,), dev),
+           _flat(dbias, "dbias", f32, (C,), dev), ws, nbytes, N, L, C, G, _act(act), code), "wkv7_group_norm_backward")
 
 
 def wkv7_get_device_status(stream=None) -> int:

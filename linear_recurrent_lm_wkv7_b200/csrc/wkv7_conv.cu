@@ -15,7 +15,14 @@ namespace wkv7 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // rows loaded before the first of them is used
+// Rows loaded before the first of them is used: enough bytes in flight for the memory's
+// latency also where an access is a single element.
+template <int VEC>
+constexpr int kAheadOf = VEC == 1 ? 8 : 4;
+// Channels per thread.  bf16: 4, not the 8 of a 16-byte access: with 8 the filter, the
+// window and the rows in flight take 140 registers or more, one block per SM (B4 T1024
+// C2304: 18.5 us against 13.0 with 4 and four blocks).
+constexpr int kVecF = 4;
 
 // Row `i` (0 .. W-2, oldest first) of the state of sequence n, or zeros.
 template <typename IO, int VEC>
@@ -34,7 +41,7 @@ __device__ __forceinline__ void load_filter(float (&wr)[W][VEC], float (&br)[VEC
     // the VEC filters are VEC * W consecutive floats
     float f[VEC * W];
     const float* src = w + static_cast<long>(c) * W;
-    if constexpr (VEC % 4 == 0) {
+    if constexpr (VEC * W % 4 == 0 && VEC > 1) {
 #pragma unroll
         for (int i = 0; i < VEC * W; i += 4) {
             const float4 v = *reinterpret_cast<const float4*>(src + i);
@@ -52,25 +59,34 @@ __device__ __forceinline__ void load_filter(float (&wr)[W][VEC], float (&br)[VEC
     }
 }
 
-// The walk over rows: sequence n with rows [lo, hi).
-struct Walk {
+// The sequences that rows of a strip belong to, one after the other.
+struct Run {
     int n;
-    long lo, hi;
+    long lo, hi;  // rows of sequence n
 };
-__device__ __forceinline__ Walk walk_start(const int32_t* offs, int B, int T, long row, int* status) {
-    Walk k;
+__device__ __forceinline__ Run run_start(const int32_t* offs, int B, int T, long row, int* status) {
+    Run k;
     k.n = offs ? seq_of_row(offs, B, row) : static_cast<int>(row / T);
     seq_span(offs, k.n, T, k.lo, k.hi, status);
     return k;
 }
-// Moves on to the sequence of `row`; true when `row` is its first.  Rows of no
-// sequence lie outside [lo, hi).
-__device__ __forceinline__ bool walk_to(Walk& k, const int32_t* offs, int B, int T, long row, int* status) {
-    while (row >= k.hi && k.n + 1 < B) {
+// The next sequence with a row at or behind `row`; false when there is none.
+__device__ __forceinline__ bool run_at(Run& k, const int32_t* offs, int B, int T, long row, int* status) {
+    while (row >= k.hi) {
+        if (k.n + 1 >= B) return false;
         ++k.n;
         seq_span(offs, k.n, T, k.lo, k.hi, status);
     }
-    return row == k.lo;
+    return true;
+}
+// Input row r of sequence k, or a row of its state where r lies before it.
+template <typename IO, int VEC, int W>
+__device__ __forceinline__ void load_before(float (&f)[VEC], const IO* x, long ldx, const IO* s0, const Run& k, long r,
+                                            int C, int c) {
+    if (r >= k.lo)
+        load_vec<VEC>(f, x + r * ldx + c);
+    else
+        load_state<IO, VEC>(f, s0, k.n, static_cast<int>(r - k.lo) + W - 1, W - 1, C, c);
 }
 
 // The last W - 1 rows of [s0; x] of sequence n, channels c ..: all read before any
@@ -96,11 +112,12 @@ __device__ void write_state(const IO* x, long ldx, const IO* s0, IO* sT, const i
 // Blocks [0, blocks_rows): y, one thread per (strip, vector of channels).  Blocks
 // after them: sT, one thread per (sequence, vector of channels).
 template <typename IO, int VEC, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 4)
     conv_fwd_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                     const IO* s0, IO* __restrict__ y, long ldy, IO* sT, const int32_t* __restrict__ offs, int B,
                     int T, long rows, int C, int act, int strip_rows, long strips, unsigned blocks_rows,
                     int* status) {
+    constexpr int kAhead = kAheadOf<VEC>;
     const int Cv = C / VEC;
     if (blockIdx.x >= blocks_rows) {
         const long i = static_cast<long>(blockIdx.x - blocks_rows) * kThreads + threadIdx.x;
@@ -115,46 +132,46 @@ __global__ void __launch_bounds__(kThreads)
 
     float wr[W][VEC], br[VEC];
     load_filter<VEC, W>(wr, br, w, bias, c);
-    Walk k = walk_start(offs, B, T, r0, status);
-    float win[W - 1][VEC];  // the rows before the current one
+    Run k = run_start(offs, B, T, r0, status);
+    for (long r = r0; r < r1 && run_at(k, offs, B, T, r, status);) {
+        if (r < k.lo) r = k.lo;  // rows before the first sequence
+        const long end = k.hi < r1 ? k.hi : r1;
+        if (r >= end) break;
+        float win[W - 1][VEC];  // the rows before the current one
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const long r = r0 - (W - 1) + j;
-        if (r >= k.lo)
-            load_vec<VEC>(win[j], x + r * ldx + c);
-        else
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) win[j][e] = 0.f;
-        if (r < k.lo && r0 > k.lo)
-            load_state<IO, VEC>(win[j], s0, k.n, static_cast<int>(r - k.lo) + W - 1, W - 1, C, c);
-    }
-    for (long r = r0; r < r1; r += kAhead) {
-        float nx[kAhead][VEC];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (r + u < r1) load_vec<VEC>(nx[u], x + (r + u) * ldx + c);
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (r + u >= r1) break;
-            if (walk_to(k, offs, B, T, r + u, status)) {
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) load_state<IO, VEC>(win[j], s0, k.n, j, W - 1, C, c);
-            }
+        for (int j = 0; j < W - 1; ++j)
+            load_before<IO, VEC, W>(win[j], x, ldx, s0, k, r - (W - 1) + j, C, c);
+        const IO* src = x + r * ldx + c;
+        IO* dst = y + r * ldy + c;
+        auto row = [&](const Raw<IO, VEC>& in) {
             float out[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 float p = br[e];
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) p = fmaf(wr[j][e], win[j][e], p);
-                out[e] = act_f32(fmaf(wr[W - 1][e], nx[u][e], p), act);
-            }
-            if (r + u >= k.lo && r + u < k.hi) store_vec<VEC>(y + (r + u) * ldy + c, out);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+                const float v = in.get(e);
+                out[e] = act_f32(fmaf(wr[W - 1][e], v, p), act);
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
-                win[W - 2][e] = nx[u][e];
+                win[W - 2][e] = v;
             }
+            store_vec<VEC>(dst, out);
+            dst += ldy;
+        };
+        for (; r + kAhead <= end; r += kAhead) {  // no branch between the rows of a batch
+            Raw<IO, VEC> nx[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) nx[u].load(src + u * ldx);
+            src += kAhead * ldx;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) row(nx[u]);
+        }
+        for (; r < end; ++r) {
+            Raw<IO, VEC> nx;
+            nx.load(src);
+            src += ldx;
+            row(nx);
         }
     }
 }
@@ -198,6 +215,7 @@ __global__ void __launch_bounds__(kThreads)
 // the strips go to the workspace, [block][(W + 1)][C], and conv_bwd_sum_kernel adds
 // the blocks in their order, so the result does not depend on timing.
 constexpr int kLanes = 32, kStrips = kThreads / kLanes;
+constexpr int kAheadB = 4;
 constexpr int kVecB = 4;  // channels per thread: x, g, w and dw windows of W rows stay in registers
 
 template <typename IO, int VEC, int W>
@@ -246,7 +264,7 @@ __device__ void write_state_grad(const IO* x, long ldx, const IO* s0, const IO* 
 }
 
 template <typename IO, int VEC, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     conv_bwd_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                     const IO* __restrict__ s0, const IO* __restrict__ dy, long lddy, const IO* __restrict__ dsT,
                     IO* __restrict__ dx, long lddx, IO* __restrict__ ds0, float* __restrict__ part,
@@ -272,83 +290,103 @@ __global__ void __launch_bounds__(kThreads)
     const long r0 = (static_cast<long>(blockIdx.x) * kStrips + sub) * strip_rows;
     const long r1 = r0 + strip_rows < rows ? r0 + strip_rows : rows;
     if (live && r0 < rows) {
-        Walk k = walk_start(offs, B, T, r0, status);
-        float xw[W][VEC], gq[W][VEC];  // rows u-W+1 .. u
-        long hq[W];                    // end row of the sequence of each of them, -1 without one
-        int nq[W];
+        Run k = run_start(offs, B, T, r0, status);
+        for (long r = r0; r < r1 && run_at(k, offs, B, T, r, status);) {
+            if (r < k.lo) r = k.lo;
+            const long end = k.hi < r1 ? k.hi : r1;
+            if (r >= end) break;
+            // g of the rows [r, last): the W - 1 behind `end` are needed for dx alone
+            const long last = end + W - 1 < k.hi ? end + W - 1 : k.hi;
+            float xw[W][VEC], gq[W][VEC];  // rows u - W + 1 .. u
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            hq[j] = -1;
-            nq[j] = 0;
-            const long r = r0 - W + j;  // one row older than needed: the first shift drops it
-            if (j > 0 && r >= k.lo) {
-                load_vec<VEC>(xw[j], x + r * ldx + c);
-            } else if (j > 0 && r0 > k.lo) {
-                load_state<IO, VEC>(xw[j], s0, k.n, static_cast<int>(r - k.lo) + W - 1, W - 1, C, c);
-            } else {
+            for (int j = 0; j < W; ++j) {
+                if (j > 0) load_before<IO, VEC, W>(xw[j], x, ldx, s0, k, r - W + j, C, c);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) xw[j][e] = 0.f;
+                for (int e = 0; e < VEC; ++e) gq[j][e] = 0.f;
             }
+            const IO *px = x + r * ldx + c, *pg = dy + r * lddy + c;
+            IO* pd = dx + r * lddx + c;
+            // row u comes in; with COUNT it belongs to the strip
+            auto step = [&](const Raw<IO, VEC>& vx, const Raw<IO, VEC>& vg, bool count) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) gq[j][e] = 0.f;
-        }
-        // rows [r0, r1) and the W - 1 after them, whose g the last dx need
-        for (long u = r0; u < r1 + W - 1; ++u) {
-            float xv[VEC], g[VEC];
-            bool valid = false;
-            if (u < rows) {
-                load_vec<VEC>(xv, x + u * ldx + c);
-                load_vec<VEC>(g, dy + u * lddy + c);
-                if (walk_to(k, offs, B, T, u, status)) {
+                for (int e = 0; e < VEC; ++e) {
 #pragma unroll
-                    for (int j = 1; j < W; ++j) load_state<IO, VEC>(xw[j], s0, k.n, j - 1, W - 1, C, c);
+                    for (int j = 0; j + 1 < W; ++j) {
+                        xw[j][e] = xw[j + 1][e];
+                        gq[j][e] = gq[j + 1][e];
+                    }
+                    xw[W - 1][e] = vx.get(e);
+                    float p = br[e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], xw[j][e], p);
+                    const float g = vg.get(e) * act_grad_f32(p, act);
+                    gq[W - 1][e] = g;
+                    if (count) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) acc[j][e] = fmaf(g, xw[j][e], acc[j][e]);
+                        acc[W][e] += g;
+                    }
                 }
-                valid = u >= k.lo && u < k.hi;
-            } else {
+            };
+            // dx of the oldest row in gq, + the gradient of the final state's row `extra`
+            auto emit = [&](const IO* extra) {
+                float d[VEC];
+                if (extra)
+                    load_vec<VEC>(d, extra);
+                else
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) xv[e] = 0.f;
-            }
+                    for (int e = 0; e < VEC; ++e) d[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-#pragma unroll
-                for (int j = 0; j + 1 < W; ++j) {
-                    xw[j][e] = xw[j + 1][e];
-                    gq[j][e] = gq[j + 1][e];
-                }
-                xw[W - 1][e] = xv[e];
-                float p = br[e];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], xw[j][e], p);
-                gq[W - 1][e] = valid ? g[e] * act_grad_f32(p, act) : 0.f;
-                if (u < r1) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        acc[j][e] = valid ? fmaf(gq[W - 1][e], xw[j][e], acc[j][e]) : acc[j][e];
-                    acc[W][e] += gq[W - 1][e];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < W; ++j) {
-                hq[j] = hq[j + 1];
-                nq[j] = nq[j + 1];
-            }
-            hq[W - 1] = valid ? k.hi : -1;
-            nq[W - 1] = k.n;
-            const long s = u - (W - 1);
-            if (s < r0 || hq[0] < 0) continue;
-            float d[VEC];
-            const long i = s - (hq[0] - (W - 1));  // row of the final state that x_s is
-            if (dsT && i >= 0)
-                load_vec<VEC>(d, dsT + (static_cast<long>(nq[0]) * (W - 1) + i) * C + c);
-            else
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) d[e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (s + j < hq[0])
+                for (int j = 0; j < W; ++j)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) d[e] = fmaf(wr[W - 1 - j][e], gq[j][e], d[e]);
-            store_vec<VEC>(dx + s * lddx + c, d);
+                store_vec<VEC>(pd, d);
+                pd += lddx;
+            };
+            long u = r;
+            auto one = [&]() {  // a row at the strip's head or tail
+                Raw<IO, VEC> vx, vg;
+                vx.load(px);
+                vg.load(pg);
+                px += ldx, pg += lddy;
+                step(vx, vg, u < end);
+                if (u - (W - 1) >= r) emit(nullptr);
+                ++u;
+            };
+            const long head = r + W - 1 < last ? r + W - 1 : last;
+            while (u < head) one();
+            for (; u + kAheadB <= end; u += kAheadB) {  // no branch between the rows of a batch
+                Raw<IO, VEC> nx[kAheadB], ng[kAheadB];
+#pragma unroll
+                for (int i = 0; i < kAheadB; ++i) {
+                    nx[i].load(px + i * ldx);
+                    ng[i].load(pg + i * lddy);
+                }
+                px += kAheadB * ldx, pg += kAheadB * lddy;
+#pragma unroll
+                for (int i = 0; i < kAheadB; ++i) {
+                    step(nx[i], ng[i], true);
+                    emit(nullptr);
+                }
+            }
+            while (u < last) one();
+            // The rows whose W - 1 followers are not all there: the sequence ends.  (Rows from
+            // hi - (W - 1) on are rows of the final state, and all of those are among them.)
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                const long s = last - (W - 1) + j;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+                    for (int i = 0; i + 1 < W; ++i) gq[i][e] = gq[i + 1][e];
+                    gq[W - 1][e] = 0.f;
+                }
+                if (s >= r && s < end) {
+                    const long i = s - (k.hi - (W - 1));
+                    emit(dsT && i >= 0 ? dsT + (static_cast<long>(k.n) * (W - 1) + i) * C + c : nullptr);
+                }
+            }
+            r = end;
         }
     }
     // sums over the block's strips, in the order of the strips
@@ -394,7 +432,8 @@ __global__ void __launch_bounds__(kThreads)
         dbias[c] = s;
 }
 
-constexpr int kBwdStripRows = 16;
+constexpr int kBwdStripRows = 32;  // the halo of W - 1 rows is read and worked on twice (16 rows: 27 us, 32: 24)
+constexpr long kWant = 512;
 
 // True when VEC-element accesses at any row and at channel multiples of VEC are aligned.
 bool vec_ok(int vec, int C, long ld0, long ld1) { return C % vec == 0 && ld0 % vec == 0 && ld1 % vec == 0; }
@@ -403,10 +442,11 @@ template <typename IO, int VEC, int W>
 cudaError_t fwd_typed(const ConvArgs& p, cudaStream_t st) {
     const int Cv = p.C / VEC;
     const long rows = p.seq_offsets ? p.T : static_cast<long>(p.B) * p.T;
-    // Rows per strip: the largest of 64, 32, 16 and 8 that still gives 1024 threads for
-    // every SM of the device (148 of them), so that enough loads are in flight.
+    // Rows per strip: the largest of 64, 32, 16 and 8 that still gives kWant threads for
+    // every SM of the device (148 of them): fewer leave too few loads in flight, more and
+    // shorter strips load filters and halos more often (1024 threads: 16 us against 13).
     int strip = 64;
-    while (strip > 8 && (rows + strip - 1) / strip * Cv < 148L * 1024) strip >>= 1;
+    while (strip > 8 && (rows + strip - 1) / strip * Cv < 148L * kWant) strip >>= 1;
     const long strips = (rows + strip - 1) / strip;
     const unsigned nb = static_cast<unsigned>((strips * Cv + kThreads - 1) / kThreads);
     const unsigned ns = p.sT ? static_cast<unsigned>((static_cast<long>(p.B) * Cv + kThreads - 1) / kThreads) : 0;
@@ -470,10 +510,10 @@ size_t conv_bwd_workspace_floats(long rows, int C, int W) {
 
 cudaError_t launch_conv(const ConvArgs& p, int io_dtype, cudaStream_t stream) {
     if (io_dtype == WKV7_BF16) {
-        if (vec_ok(8, p.C, p.ldx, p.ldy)) WKV7_CONV_WIDTHS(fwd_typed, __nv_bfloat16, 8)
+        if (vec_ok(kVecF, p.C, p.ldx, p.ldy)) WKV7_CONV_WIDTHS(fwd_typed, __nv_bfloat16, kVecF)
         WKV7_CONV_WIDTHS(fwd_typed, __nv_bfloat16, 1)
     }
-    if (vec_ok(4, p.C, p.ldx, p.ldy)) WKV7_CONV_WIDTHS(fwd_typed, float, 4)
+    if (vec_ok(kVecF, p.C, p.ldx, p.ldy)) WKV7_CONV_WIDTHS(fwd_typed, float, kVecF)
     WKV7_CONV_WIDTHS(fwd_typed, float, 1)
 }
 

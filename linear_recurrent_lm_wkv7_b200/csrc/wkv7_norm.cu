@@ -55,111 +55,139 @@ __device__ __forceinline__ void load_param(float (&f)[VEC], const float* p, int 
 }
 
 // ---------------------------------------------------------------- row form
-// Unit u = row * G + group.  A team's lane holds vectors lane, lane + TEAM, .. of the
-// group: K of them.
+// A team stays on one group and walks rows, with the parameters in registers and the
+// next row's vectors already on their way.  Block (bx, by): groups bx * gpb .., rows
+// by * rpb + team row, in steps of gridDim.y * rpb; gpb * rpb teams in the block.  A
+// team's lane holds vectors lane, lane + TEAM, .. of the group: K of them.
+struct RowPlace {
+    int lane, g, trow, rpb;
+    bool member;
+};
+template <int TEAM>
+__device__ __forceinline__ RowPlace row_place(int gpb, int G) {
+    RowPlace p;
+    p.lane = threadIdx.x % TEAM;
+    const int team = threadIdx.x / TEAM;
+    p.rpb = kThreads / TEAM / gpb;
+    p.g = blockIdx.x * gpb + team % gpb;
+    p.trow = team / gpb;
+    p.member = p.trow < p.rpb && p.g < G;
+    return p;
+}
+
 template <typename IO, int VEC, int TEAM, int K>
 __global__ void __launch_bounds__(kThreads)
     norm_row_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
-                    const float* __restrict__ bias, IO* __restrict__ y, long ldy, float* __restrict__ stats,
-                    long units, int G, int Cg, float eps, int act) {
+                    const float* __restrict__ bias, IO* __restrict__ y, long ldy, float* __restrict__ stats, long N,
+                    int G, int Cg, int gpb, float eps, int act) {
     __shared__ float red[TEAM > 32 ? TEAM / 32 : 1];
-    const int lane = threadIdx.x % TEAM;
-    const long u = static_cast<long>(blockIdx.x) * (kThreads / TEAM) + threadIdx.x / TEAM;
-    const bool live = u < units;  // a whole team is live or not; teams past the end still take part in shuffles
-    const long row = live ? u / G : 0;
-    const int g = live ? static_cast<int>(u % G) : 0;
-    const int nv = Cg / VEC;
-    float v[K][VEC];
-    float s = 0.f;
+    const RowPlace p = row_place<TEAM>(gpb, G);
+    const int nv = Cg / VEC, c0 = p.g * Cg + p.lane * VEC;
+    const float inv = 1.f / Cg;
+    float wv[K][VEC], bv[K][VEC];
+    Raw<IO, VEC> nx[K];
+    const long step = static_cast<long>(gridDim.y) * p.rpb;
+    long row = static_cast<long>(blockIdx.y) * p.rpb + p.trow;
+    auto fetch = [&](long r) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = lane + k * TEAM;
-        if (live && i < nv) {
-            load_vec<VEC>(v[k], x + row * ldx + static_cast<long>(g) * Cg + i * VEC);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s += v[k][e];
-        }
-    }
-    const float mean = team_sum<TEAM>(s, red) / Cg;
-    s = 0.f;
+        for (int k = 0; k < K; ++k)
+            if (p.member && r < N && p.lane + k * TEAM < nv) nx[k].load(x + r * ldx + c0 + k * TEAM * VEC);
+    };
+    fetch(row);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (live && lane + k * TEAM < nv)
+        if (p.member && p.lane + k * TEAM < nv) {
+            load_param<VEC>(wv[k], weight, c0 + k * TEAM * VEC, 1.f);
+            load_param<VEC>(bv[k], bias, c0 + k * TEAM * VEC, 0.f);
+        }
+    // every thread of the block takes the same number of turns: team_sum is collective
+    for (long r0 = static_cast<long>(blockIdx.y) * p.rpb; r0 < N; r0 += step, row += step) {
+        const bool live = p.member && row < N;
+        float v[K][VEC], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool mine = live && p.lane + k * TEAM < nv;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                v[k][e] -= mean;
-                s = fmaf(v[k][e], v[k][e], s);
+                v[k][e] = mine ? nx[k].get(e) : 0.f;
+                s += v[k][e];
             }
-    const float rstd = rstd_of(team_sum<TEAM>(s, red) / Cg, eps);
-    if (!live) return;
-    if (stats && lane == 0) {
-        stats[2 * u] = mean;
-        stats[2 * u + 1] = rstd;
-    }
+        }
+        fetch(row + step);
+        const float mean = team_sum<TEAM>(s, red) * inv;
+        s = 0.f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int i = lane + k * TEAM;
-        if (i >= nv) continue;
-        const int c = g * Cg + i * VEC;
-        float wv[VEC], bv[VEC], out[VEC];
-        load_param<VEC>(wv, weight, c, 1.f);
-        load_param<VEC>(bv, bias, c, 0.f);
+        for (int k = 0; k < K; ++k)
+            if (p.lane + k * TEAM < nv)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) out[e] = act_f32(fmaf(v[k][e] * rstd, wv[e], bv[e]), act);
-        store_vec<VEC>(y + row * ldy + c, out);
+                for (int e = 0; e < VEC; ++e) {
+                    v[k][e] -= mean;
+                    s = fmaf(v[k][e], v[k][e], s);
+                }
+        const float rstd = rstd_of(team_sum<TEAM>(s, red) * inv, eps);
+        if (!live) continue;
+        if (stats && p.lane == 0)
+            *reinterpret_cast<float2*>(stats + 2 * (row * G + p.g)) = make_float2(mean, rstd);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (p.lane + k * TEAM >= nv) continue;
+            float out[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) out[e] = act_f32(fmaf(v[k][e] * rstd, wv[k][e], bv[k][e]), act);
+            store_vec<VEC>(y + row * ldy + c0 + k * TEAM * VEC, out);
+        }
     }
 }
 
-// The backward keeps a team on one group and walks rows, so that the sums of dweight
-// and dbias over the rows stay in registers.  Block (bx, by): groups bx * gpb ..,
-// rows by * rpb + team row, in steps of gridDim.y * rpb; gpb * rpb teams in the block.
-// The block's sums go to part [by][2][C].
+// The sums of dweight and dbias over a team's rows stay in registers; the block's go to
+// part [by][2][C].
 template <typename IO, int VEC, int TEAM, int K>
 __global__ void __launch_bounds__(kThreads)
     norm_row_bwd_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
                         const float* __restrict__ bias, const float* __restrict__ stats, const IO* __restrict__ dy,
                         long lddy, IO* __restrict__ dx, long lddx, float* __restrict__ part, long N, int G, int Cg,
                         int gpb, int act) {
-    constexpr int TEAMS = kThreads / TEAM;
     __shared__ float red[TEAM > 32 ? TEAM / 32 : 1];
     __shared__ float sums[kThreads * VEC];
-    const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
-    const int rpb = TEAMS / gpb;
-    const int g = blockIdx.x * gpb + team % gpb, trow = team / gpb;
-    const bool member = trow < rpb && g < G;
-    const int nv = Cg / VEC;
+    const RowPlace p = row_place<TEAM>(gpb, G);
+    const int nv = Cg / VEC, c0 = p.g * Cg + p.lane * VEC;
+    const float inv = 1.f / Cg;
     float wv[K][VEC], bv[K][VEC], aw[K][VEC], ab[K][VEC];
+    Raw<IO, VEC> nx[K], ny[K];
+    float2 ns = make_float2(0.f, 0.f);
+    const long step = static_cast<long>(gridDim.y) * p.rpb;
+    long row = static_cast<long>(blockIdx.y) * p.rpb + p.trow;
+    auto fetch = [&](long r) {
+        if (!p.member || r >= N) return;
+        ns = *reinterpret_cast<const float2*>(stats + 2 * (r * G + p.g));
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (p.lane + k * TEAM < nv) {
+                nx[k].load(x + r * ldx + c0 + k * TEAM * VEC);
+                ny[k].load(dy + r * lddy + c0 + k * TEAM * VEC);
+            }
+    };
+    fetch(row);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int i = lane + k * TEAM;
-        if (member && i < nv) {
-            load_param<VEC>(wv[k], weight, g * Cg + i * VEC, 1.f);
-            load_param<VEC>(bv[k], bias, g * Cg + i * VEC, 0.f);
+        if (p.member && p.lane + k * TEAM < nv) {
+            load_param<VEC>(wv[k], weight, c0 + k * TEAM * VEC, 1.f);
+            load_param<VEC>(bv[k], bias, c0 + k * TEAM * VEC, 0.f);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) aw[k][e] = ab[k][e] = 0.f;
     }
-    const long step = static_cast<long>(gridDim.y) * rpb;
-    // every thread of the block takes the same number of turns: team_sum is collective
-    for (long r0 = static_cast<long>(blockIdx.y) * rpb; r0 < N; r0 += step) {
-        const long row = r0 + trow;
-        const bool live = member && row < N;
-        float mean = 0.f, rstd = 0.f, h[K][VEC], q[K][VEC], s1 = 0.f, s2 = 0.f;
-        if (live) {
-            mean = stats[2 * (row * G + g)];
-            rstd = stats[2 * (row * G + g) + 1];
-        }
+    for (long r0 = static_cast<long>(blockIdx.y) * p.rpb; r0 < N; r0 += step, row += step) {
+        const bool live = p.member && row < N;
+        const float mean = ns.x, rstd = ns.y;
+        float h[K][VEC], q[K][VEC], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int i = lane + k * TEAM;
-            if (!live || i >= nv) continue;
-            const int c = g * Cg + i * VEC;
-            load_vec<VEC>(h[k], x + row * ldx + c);
-            load_vec<VEC>(q[k], dy + row * lddy + c);
+            if (!live || p.lane + k * TEAM >= nv) continue;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                h[k][e] = (h[k][e] - mean) * rstd;
-                q[k][e] *= act_grad_f32(fmaf(h[k][e], wv[k][e], bv[k][e]), act);
+                h[k][e] = (nx[k].get(e) - mean) * rstd;
+                q[k][e] = ny[k].get(e) * act_grad_f32(fmaf(h[k][e], wv[k][e], bv[k][e]), act);
                 ab[k][e] += q[k][e];
                 aw[k][e] = fmaf(q[k][e], h[k][e], aw[k][e]);
                 q[k][e] *= wv[k][e];
@@ -167,20 +195,21 @@ __global__ void __launch_bounds__(kThreads)
                 s2 = fmaf(q[k][e], h[k][e], s2);
             }
         }
-        const float m1 = team_sum<TEAM>(s1, red) / Cg;
-        const float m2 = team_sum<TEAM>(s2, red) / Cg;
+        fetch(row + step);
+        const float m1 = team_sum<TEAM>(s1, red) * inv;
+        const float m2 = team_sum<TEAM>(s2, red) * inv;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int i = lane + k * TEAM;
-            if (!live || i >= nv) continue;
+            if (!live || p.lane + k * TEAM >= nv) continue;
             float d[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) d[e] = rstd * (q[k][e] - m1 - h[k][e] * m2);
-            store_vec<VEC>(dx + row * lddx + static_cast<long>(g) * Cg + i * VEC, d);
+            store_vec<VEC>(dx + row * lddx + c0 + k * TEAM * VEC, d);
         }
     }
     // the block's sums: team rows in order
     const long C = static_cast<long>(G) * Cg;
+    const int col = threadIdx.x / TEAM % gpb;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -189,36 +218,39 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) sums[threadIdx.x * VEC + e] = which ? ab[k][e] : aw[k][e];
             __syncthreads();
-            const int i = lane + k * TEAM;
-            if (trow != 0 || !member || i >= nv) continue;
+            if (p.trow != 0 || !p.member || p.lane + k * TEAM >= nv) continue;
             float s[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[e] = 0.f;
-            for (int t = 0; t < rpb; ++t)
+            for (int t = 0; t < p.rpb; ++t)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[e] += sums[((t * gpb + team) * TEAM + lane) * VEC + e];
-            store_vec<VEC>(part + (static_cast<long>(blockIdx.y) * 2 + which) * C + g * Cg + i * VEC, s);
+                for (int e = 0; e < VEC; ++e) s[e] += sums[((t * gpb + col) * TEAM + p.lane) * VEC + e];
+            store_vec<VEC>(part + (static_cast<long>(blockIdx.y) * 2 + which) * C + c0 + k * TEAM * VEC, s);
         }
 }
 
-// out [2][C] = dweight, dbias: the partials [nblk][2][C] added in the order of the blocks.
-__global__ void __launch_bounds__(kThreads)
+// out [2][C] = dweight, dbias: the partials [nblk][2][C] added in a fixed order: 32
+// columns a block, every 32nd partial a thread, then the 32 sums.
+__global__ void __launch_bounds__(1024)
     norm_sum_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db, long nblk,
                     long C) {
-    __shared__ float red[8][32];
+    __shared__ float red[32][33];
     const int lane = threadIdx.x % 32, sub = threadIdx.x / 32;
     const long col = static_cast<long>(blockIdx.x) * 32 + lane;
     float s = 0.f;
-    if (col < 2 * C)
-        for (long b = sub; b < nblk; b += 8) s += part[b * 2 * C + col];
+    if (col < 2 * C) {
+#pragma unroll 8
+        for (long b = sub; b < nblk; b += 32) s += part[b * 2 * C + col];
+    }
     red[sub][lane] = s;
     __syncthreads();
-    if (sub != 0 || col >= 2 * C) return;
-    s = 0.f;
+    s = red[lane][sub];  // warp `sub` adds column `sub`
 #pragma unroll
-    for (int t = 0; t < 8; ++t) s += red[t][lane];
-    float* dst = col < C ? dw : db;
-    if (dst) dst[col < C ? col : col - C] = s;
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(kFull, s, m);
+    const long out = static_cast<long>(blockIdx.x) * 32 + sub;
+    if (lane != 0 || out >= 2 * C) return;
+    float* dst = out < C ? dw : db;
+    if (dst) dst[out < C ? out : out - C] = s;
 }
 
 // ---------------------------------------------------------------- split form
@@ -279,7 +311,6 @@ __global__ void __launch_bounds__(kThreads)
     // one warp per group of the tile: its members' moments, lane by lane, then across lanes
     const int cend = min(c0 + lanes * VEC, C);
     const int warp = threadIdx.x / 32, ln = threadIdx.x % 32;
-    const long slot = (static_cast<long>(blockIdx.y) * gridDim.x + blockIdx.x) * gridDim.z + blockIdx.z;
     const int G = C / Cg;
     for (int g = c0 / Cg + warp; g * Cg < cend; g += kThreads / 32) {
         const int a = (max(g * Cg, c0) - c0) / VEC, b = (min((g + 1) * Cg, cend) - c0) / VEC;
@@ -293,56 +324,80 @@ __global__ void __launch_bounds__(kThreads)
             t = merge(t, o);
         }
         if (ln == 0) {
-            float* p = part + (slot * G + g) * 3;
+            // [sample][group][tile][split]: what one group is joined from lies together
+            float* p = part + (((static_cast<long>(blockIdx.y) * G + g) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) * 3;
             p[0] = t.n, p[1] = t.mean, p[2] = t.m2;
         }
     }
 }
 
-// mean and rstd of every (sample, group) from the moments of its splits and tiles.
+// Mean and rstd of sample n's group g from the moments of its splits, in the tiles that
+// hold it: a whole warp.
+__device__ __forceinline__ float2 join_moments(const float* part, long n, int g, int G, int Cg, int splits, int tiles,
+                                               int tile_c, float eps, int ln) {
+    const int z0 = g * Cg / tile_c, z1 = ((g + 1) * Cg - 1) / tile_c, nz = z1 - z0 + 1;
+    const float* base = part + (((n * G + g) * tiles + z0) * splits) * 3;
+    // the mean, then the squares about it: no chain of merges, each with a division
+    float cnt = 0.f, sum = 0.f, m2 = 0.f;
+#pragma unroll 4
+    for (int i = ln; i < splits * nz; i += 32) {
+        cnt += base[3 * i];
+        sum = fmaf(base[3 * i], base[3 * i + 1], sum);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+        cnt += __shfl_xor_sync(kFull, cnt, d);
+        sum += __shfl_xor_sync(kFull, sum, d);
+    }
+    const float mean = sum / cnt;
+#pragma unroll 4
+    for (int i = ln; i < splits * nz; i += 32) {
+        const float d = base[3 * i + 1] - mean;
+        m2 += fmaf(base[3 * i] * d, d, base[3 * i + 2]);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m2 += __shfl_xor_sync(kFull, m2, d);
+    return make_float2(mean, rstd_of(m2 / cnt, eps));
+}
+
+// The statistics of every (sample, group), a warp each.
 __global__ void __launch_bounds__(kThreads)
     norm_join_kernel(const float* __restrict__ part, float* __restrict__ stats, long units, int G, int Cg, int splits,
                      int tiles, int tile_c, float eps) {
     const long u = static_cast<long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-    const int ln = threadIdx.x % 32;
     if (u >= units) return;
-    const long n = u / G;
-    const int g = static_cast<int>(u % G);
-    const int z0 = g * Cg / tile_c, z1 = ((g + 1) * Cg - 1) / tile_c;  // the tiles that hold the group
-    const int nz = z1 - z0 + 1;
-    Moments t{0.f, 0.f, 0.f};
-    for (int i = ln; i < splits * nz; i += 32) {
-        const long slot = (n * splits + i / nz) * tiles + z0 + i % nz;
-        const float* p = part + (slot * G + g) * 3;
-        t = merge(t, Moments{p[0], p[1], p[2]});
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-        const Moments o{__shfl_down_sync(kFull, t.n, d), __shfl_down_sync(kFull, t.mean, d),
-                        __shfl_down_sync(kFull, t.m2, d)};
-        t = merge(t, o);
-    }
-    if (ln == 0) {
-        stats[2 * u] = t.mean;
-        stats[2 * u + 1] = rstd_of(t.m2 / t.n, eps);
-    }
+    const float2 s = join_moments(part, u / G, static_cast<int>(u % G), G, Cg, splits, tiles, tile_c, eps,
+                                  threadIdx.x % 32);
+    if (threadIdx.x % 32 == 0) *reinterpret_cast<float2*>(stats + 2 * u) = s;
 }
 
-// y from x and the statistics; thread: one vector of channels, rows prow, prow + par, ..
-// of the split.  Groups of a vector's elements may differ, so each takes its own.
-template <typename IO, int VEC>
+// y from x and the statistics; thread: one vector of channels (all of one group: VEC
+// divides Cg or is 1), rows prow, prow + par, .. of the split.  JOIN: every block joins the
+// moments of its tile's groups itself, and the first split writes the statistics.
+template <typename IO, int VEC, bool JOIN>
 __global__ void __launch_bounds__(kThreads)
     norm_apply_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
-                      const float* __restrict__ bias, const float* __restrict__ stats, IO* __restrict__ y, long ldy,
-                      long L, int C, int Cg, int lanes, long split_rows, int act) {
+                      const float* __restrict__ bias, float* __restrict__ stats, IO* __restrict__ y, long ldy, long L,
+                      int C, int Cg, int lanes, long split_rows, int act, const float* __restrict__ part, float eps) {
+    __shared__ float2 joined[JOIN ? kThreads * VEC : 1];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
-    const int c = (blockIdx.z * lanes + lane) * VEC;
+    const int c0 = blockIdx.z * lanes * VEC, c = c0 + lane * VEC, G = C / Cg;
+    const long n = blockIdx.y;
+    if constexpr (JOIN) {
+        const int cend = min(c0 + lanes * VEC, C), g0 = c0 / Cg;
+        for (int g = g0 + threadIdx.x / 32; g * Cg < cend; g += kThreads / 32) {
+            const float2 s = join_moments(part, n, g, G, Cg, gridDim.x, gridDim.z, lanes * VEC, eps, threadIdx.x % 32);
+            if (threadIdx.x % 32 == 0) {
+                joined[g - g0] = s;
+                if (stats && blockIdx.x == 0) *reinterpret_cast<float2*>(stats + 2 * (n * G + g)) = s;
+            }
+        }
+        __syncthreads();
+    }
     if (prow >= par || c >= C) return;
     const long l0 = static_cast<long>(blockIdx.x) * split_rows;
     const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
-    const long n = blockIdx.y;
-    const int g = c / Cg;  // VEC divides Cg or is 1
-    const float mean = stats[2 * (n * (C / Cg) + g)], rstd = stats[2 * (n * (C / Cg) + g) + 1];
+    const float2 st = JOIN ? joined[c / Cg - c0 / Cg] : *reinterpret_cast<const float2*>(stats + 2 * (n * G + c / Cg));
     float wv[VEC], bv[VEC];
     load_param<VEC>(wv, weight, c, 1.f);
     load_param<VEC>(bv, bias, c, 0.f);
@@ -353,7 +408,7 @@ __global__ void __launch_bounds__(kThreads)
         float v[VEC];
         load_vec<VEC>(v, src + l * ldx);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = act_f32(fmaf((v[e] - mean) * rstd, wv[e], bv[e]), act);
+        for (int e = 0; e < VEC; ++e) v[e] = act_f32(fmaf((v[e] - st.x) * st.y, wv[e], bv[e]), act);
         store_vec<VEC>(dst + l * ldy, v);
     }
 }
@@ -478,7 +533,8 @@ bool vec_ok(int Cg, long a, long b, long c) {
 }
 
 // How the split form cuts [N][L][C]: `lanes` vectors of channels per tile, and splits
-// of the rows.  The partials' number is bounded by 8 per SM or one per 16 rows.
+// of the rows: some kSplitPerSm blocks for every SM, of 16 rows a thread at least.
+constexpr int kSplitPerSm = 2;
 struct Split {
     int lanes, tiles, splits;
     long split_rows;
@@ -489,7 +545,7 @@ Split split_of(long N, long L, int C, int vec) {
     s.lanes = nv < kThreads ? nv : kThreads;
     s.tiles = (nv + s.lanes - 1) / s.lanes;
     const int par = kThreads / s.lanes;
-    const long want = (148L * 8 + N * s.tiles - 1) / (N * s.tiles);
+    const long want = (148L * kSplitPerSm + N * s.tiles - 1) / (N * s.tiles);
     const long most = (L + 16L * par - 1) / (16L * par);
     const long n = want < most ? want : most;
     s.split_rows = (L + n - 1) / n;
@@ -510,23 +566,27 @@ int team_of(int nv) {
 }
 int team_threads(int team) { return team <= 32 ? team : team <= 128 ? 32 : 256; }
 
-// Blocks of rows in the row form's backward: two blocks per SM share the column of
-// groups, each with at least one turn.
-struct RowBwd {
+// The row form's grid: `per_sm` blocks for every SM share the rows, each with at least
+// one turn.  Forward: what is resident at once.  Backward: fewer, as every block leaves
+// two rows of partial sums.
+struct RowGrid {
     int gpb, gx;
     long gy;
 };
-RowBwd row_bwd_of(long N, int G, int team) {
-    RowBwd r;
+RowGrid row_grid_of(long N, int G, int team, int per_sm) {
+    RowGrid r;
     const int teams = kThreads / team_threads(team);
     r.gpb = G < teams ? G : teams;
     r.gx = (G + r.gpb - 1) / r.gpb;
     const int rpb = teams / r.gpb;
-    long gy = (148L * 4 + r.gx - 1) / r.gx;
+    long gy = (148L * per_sm + r.gx - 1) / r.gx;
     const long most = (N + rpb - 1) / rpb;
     r.gy = gy < most ? gy : most;
     return r;
 }
+
+constexpr int kPerSmFwd = 4, kPerSmBwd = 2;
+constexpr long kJoinMost = 8192;
 
 #define WKV7_NORM_TEAMS(CALL)              \
     switch (team) {                        \
@@ -550,11 +610,11 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
     const long units = static_cast<long>(p.N) * p.G;
     const int team = p.L == 1 ? team_of(Cg / VEC) : 0;
     if (team) {
-        const int per = kThreads / team_threads(team);
-        const unsigned blocks = static_cast<unsigned>((units + per - 1) / per);
-#define CALL(TEAM, K)                                                                                              \
-    norm_row_kernel<IO, VEC, TEAM, K><<<blocks, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, y, p.ldy, p.stats,  \
-                                                                   units, p.G, Cg, p.eps, p.act)
+        const RowGrid r = row_grid_of(p.N, p.G, team, kPerSmFwd);
+        const dim3 grid(r.gx, static_cast<unsigned>(r.gy));
+#define CALL(TEAM, K)                                                                                            \
+    norm_row_kernel<IO, VEC, TEAM, K><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, y, p.ldy, p.stats,  \
+                                                                 p.N, p.G, Cg, r.gpb, p.eps, p.act)
         WKV7_NORM_TEAMS(CALL)
 #undef CALL
         return cudaGetLastError();
@@ -564,10 +624,21 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
     float* stats = p.stats ? p.stats : part + static_cast<size_t>(p.N) * s.splits * s.tiles * p.G * 3;
     const dim3 grid(s.splits, p.N, s.tiles);
     norm_stats_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, part, p.L, p.C, Cg, s.lanes, s.split_rows);
-    norm_join_kernel<<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, st>>>(
-        part, stats, units, p.G, Cg, s.splits, s.tiles, s.lanes * VEC, p.eps);
-    norm_apply_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, stats, y, p.ldy, p.L, p.C, Cg,
-                                                          s.lanes, s.split_rows, p.act);
+    // A launch less where the blocks can join the moments on the side: up to kJoinMost of
+    // them each (45 groups of 132 splits, fp32 [3][2111][960]: 15.5 us against 23 with a
+    // launch for the join).
+    const int tile_groups = (s.lanes * VEC + Cg - 1) / Cg + 1;
+    if (static_cast<long>(tile_groups) * s.splits * ((Cg + s.lanes * VEC - 1) / (s.lanes * VEC) + 1) <= kJoinMost) {
+        norm_apply_kernel<IO, VEC, true><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, y, p.ldy, p.L,
+                                                                    p.C, Cg, s.lanes, s.split_rows, p.act, part,
+                                                                    p.eps);
+    } else {
+        norm_join_kernel<<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, st>>>(
+            part, stats, units, p.G, Cg, s.splits, s.tiles, s.lanes * VEC, p.eps);
+        norm_apply_kernel<IO, VEC, false><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, stats, y, p.ldy, p.L,
+                                                                     p.C, Cg, s.lanes, s.split_rows, p.act, nullptr,
+                                                                     p.eps);
+    }
     return cudaGetLastError();
 }
 
@@ -581,7 +652,7 @@ cudaError_t norm_bwd_typed(const NormBwdArgs& p, cudaStream_t st) {
     if (p.N == 0 || p.L == 0) {
         nblk = 0;  // no rows: dweight and dbias are zero
     } else if (team) {
-        const RowBwd r = row_bwd_of(p.N, p.G, team);
+        const RowGrid r = row_grid_of(p.N, p.G, team, kPerSmBwd);
         const dim3 grid(r.gx, static_cast<unsigned>(r.gy));
         nblk = r.gy;
 #define CALL(TEAM, K)                                                                                             \
@@ -604,7 +675,7 @@ cudaError_t norm_bwd_typed(const NormBwdArgs& p, cudaStream_t st) {
                                                                   s.split_rows, p.act);
     }
     if (p.dw || p.db)
-        norm_sum_kernel<<<static_cast<unsigned>((2L * p.C + 31) / 32), kThreads, 0, st>>>(p.ws, p.dw, p.db, nblk,
+        norm_sum_kernel<<<static_cast<unsigned>((2L * p.C + 31) / 32), 1024, 0, st>>>(p.ws, p.dw, p.db, nblk,
                                                                                           p.C);
     return cudaGetLastError();
 }
@@ -620,7 +691,7 @@ size_t ws_floats(int N, int L, int C, int G, bool backward) {
         const int team = L == 1 ? team_of(Cg / vec) : 0;
         size_t n = 0;
         if (team) {
-            if (backward) n = static_cast<size_t>(row_bwd_of(N, G, team).gy) * 2 * C;
+            if (backward) n = static_cast<size_t>(row_grid_of(N, G, team, kPerSmBwd).gy) * 2 * C;
         } else {
             const Split s = split_of(N, L, C, vec);
             n = backward ? static_cast<size_t>(N) * s.splits * 2 * C + static_cast<size_t>(N) * G * 2
