@@ -45,9 +45,15 @@ struct SegMap {
 inline __host__ __device__ long seg_slots(const SegMap& m) {
     return m.offs ? m.T / m.seg + m.B : static_cast<long>(m.B) * m.spb;
 }
-// The cut that the scan uses for a problem (wkv7_scan.cu): one segment per sequence
-// (seg >= T) where sequences and heads fill the device.
-SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed);
+// How a kernel that carries one head's state through chunks is best cut (wkv7_scan.cu).
+struct CutCost {
+    int chunk;       // tokens per chunk
+    int resident;    // blocks that run at once
+    double states;   // time of a chunk in the pass that only makes states, of a chunk's otherwise
+    double start;    // time before a block's first chunk, in chunks
+    double join;     // of the join and the launches, in chunks
+};
+SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed, const CutCost& cost);
 __device__ __forceinline__ long seg_first(const SegMap& m, int n, long lo) {
     return m.offs ? lo / m.seg + n : static_cast<long>(n) * m.spb;
 }

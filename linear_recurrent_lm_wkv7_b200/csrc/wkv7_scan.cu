@@ -18,6 +18,11 @@
 #include "scan_common.cuh"
 
 namespace wkv7 {
+
+// wkv7_scan_tc.cu: one pass of the tcgen05 kernel, over the outputs or the segments' states
+cudaError_t launch_scan_tc(const ScanArgs& p, const SegMap& map, bool whole, bool out, float* seg_state,
+                           float* seg_decay, cudaStream_t stream);
+
 namespace {
 
 template <typename IO, int N>
@@ -431,21 +436,13 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Segments per sequence: enough to give every SM two blocks, when the sequences and
-// heads alone leave SMs idle for longer than the first pass over the segments costs
-// (it does less than half of the second's products).
-int segments_of(long units, long tokens_per_seq) {
-    const long chunks = (tokens_per_seq + kChunk - 1) / kChunk;
-    constexpr long kSms = 148;
-    if (units >= 2 * kSms) return 1;
-    const long want = 2 * kSms / units;
-    if (want < 2) return 1;
-    const long waves = (units + kSms - 1) / kSms;
-    // chunk times on the critical path, one block per SM: one pass against both, plus
-    // some eight chunk times for the two extra launches
-    if (3 * chunks * units / (2 * kSms) + 8 >= chunks * waves) return 1;
-    return static_cast<int>(want < chunks ? want : chunks);
-}
+// The two kernels: this file's on warp-level products, two blocks per SM, and
+// wkv7_scan_tc.cu's.  Chunk times measured at B4 T1024 H32 N128 and B1 T16384 H40 N128.
+constexpr CutCost kCutWarp{kChunk, 296, 0.5, 1.0, 2.0};
+constexpr CutCost kCutTc{128, 148, 0.45, 1.5, 4.0};
+// bf16 with N = 128 runs on the tcgen05 kernel (its tiles are 128 columns wide; rows are
+// numbered in 31 bits there).
+bool uses_tc(int io_dtype, int N, long rows) { return io_dtype == WKV7_BF16 && N == 128 && rows < (1L << 31); }
 
 template <typename IO, int N>
 cudaError_t scan_typed(const ScanArgs& p, const SegMap& map, bool whole, ScanDev& d, cudaStream_t st) {
@@ -467,34 +464,65 @@ cudaError_t scan_typed(const ScanArgs& p, const SegMap& map, bool whole, ScanDev
 
 }  // namespace
 
-SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed) {
+// Sequences are cut into S segments where that is faster: blocks of one segment each run
+// in waves, and a cut needs a pass over the states and the join first.
+SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed, const CutCost& k) {
     SegMap m{offs, B, T, 0, 1};
-    const long per = packed ? (T + B - 1) / B : T;
-    const int want = segments_of(static_cast<long>(B) * H, per);
-    if (want <= 1) {
-        m.seg = (T + kChunk - 1) / kChunk * kChunk;
-        if (m.seg == 0) m.seg = kChunk;
+    const long per = packed ? (T + B - 1) / B : T, units = static_cast<long>(B) * H;
+    const long chunks = (per + k.chunk - 1) / k.chunk;
+    auto waves = [&](long blocks) { return static_cast<double>((blocks + k.resident - 1) / k.resident); };
+    long best = 1;
+    double least = waves(units) * (chunks + k.start);
+    for (long s = 2; s <= chunks && s <= 64 && units * s <= 8L * k.resident; ++s) {
+        const long c = (chunks + s - 1) / s;
+        const double t = waves(units * s) * (c * (1.0 + k.states) + 2 * k.start) + k.join;
+        if (t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    if (best == 1) {
+        m.seg = (static_cast<long>(T) + k.chunk - 1) / k.chunk * k.chunk;
+        if (m.seg == 0) m.seg = k.chunk;
         return m;
     }
-    const long chunks = (per + kChunk - 1) / kChunk;
-    m.seg = (chunks + want - 1) / want * kChunk;
+    m.seg = (chunks + best - 1) / best * k.chunk;
     m.spb = static_cast<int>((T + m.seg - 1) / m.seg);
     return m;
 }
 
-size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
-    const SegMap m = scan_segments(B, T, H, nullptr, packed);
+static size_t cut_bytes(int B, int T, int H, int N, bool packed, const CutCost& cost) {
+    const SegMap m = scan_segments(B, T, H, nullptr, packed, cost);
     if (m.seg >= T) return 0;
     const long slots = packed ? T / m.seg + B : static_cast<long>(B) * m.spb;
     return static_cast<size_t>(slots) * H * (static_cast<size_t>(kScanP) * N + 4) * sizeof(float);
 }
 
+// Of either kernel: the size query does not know the io type.
+size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
+    const size_t w = cut_bytes(B, T, H, N, packed, kCutWarp);
+    const size_t t = N == 128 ? cut_bytes(B, T, H, N, packed, kCutTc) : 0;
+    return w > t ? w : t;
+}
+
 cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
-    const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, p.seq_offsets != nullptr);
+    const bool tc = uses_tc(io_dtype, p.N, p.seq_offsets ? p.T : static_cast<long>(p.B) * p.T);
+    const SegMap map =
+        scan_segments(p.B, p.T, p.H, p.seq_offsets, p.seq_offsets != nullptr, tc ? kCutTc : kCutWarp);
     const bool whole = map.seg >= p.T;
     ScanDev d{p.x, p.dt, p.Bm, p.Cm, p.ldx, p.lddt, p.ldb, p.ldc, p.ldy, p.A, p.D, p.dt_bias, p.s0, p.y, p.sT,
-              p.ws, p.ws ? p.ws + static_cast<size_t>(seg_slots(map)) * p.H * kScanP * p.N : nullptr, p.H, p.G,
+              p.ws, whole ? nullptr : p.ws + static_cast<size_t>(seg_slots(map)) * p.H * kScanP * p.N, p.H, p.G,
               p.softplus, p.dt_dtype == WKV7_BF16, map, p.status};
+    if (tc) {
+        cudaError_t e = cudaSuccess;
+        if (!whole) {
+            e = launch_scan_tc(p, map, false, false, d.seg_state, d.seg_decay, stream);
+            if (e != cudaSuccess) return e;
+            constexpr int elems = kScanP * 128;
+            scan_join_kernel<<<dim3(static_cast<unsigned>(p.B) * p.H, elems / 4 / 256), 256, 0, stream>>>(d, elems);
+        }
+        return launch_scan_tc(p, map, whole, true, d.seg_state, d.seg_decay, stream);
+    }
     if (io_dtype == WKV7_BF16) switch (p.N) {
             case 16: return scan_typed<__nv_bfloat16, 16>(p, map, whole, d, stream);
             case 32: return scan_typed<__nv_bfloat16, 32>(p, map, whole, d, stream);

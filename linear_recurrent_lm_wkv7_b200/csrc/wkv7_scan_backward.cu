@@ -851,7 +851,8 @@ struct Plan {
 };
 Plan plan_of(int B, int T, int H, int N, int G, int io_dtype, const int32_t* offs, bool packed) {
     Plan p;
-    p.seg = scan_segments(B, T, 2 * H, offs, packed);  // both directions run at once
+    // both directions run at once; without segments the one pass makes states anyway
+    p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, 296, 1.0, 1.0, 2.0});
     p.whole = p.seg.seg >= T;
     p.chunk = SegMap{offs, B, T, kChunk, (T + kChunk - 1) / kChunk};
     p.seg_count = packed ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;

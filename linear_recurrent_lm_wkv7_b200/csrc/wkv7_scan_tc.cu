@@ -1,0 +1,603 @@
+// wkv7_scan_tc.cu — selective scan of bf16 prompts with N = 128 on the tcgen05 tensor
+// cores.  The recurrence, its chunk form and the decays: scan_common.cuh; here a chunk
+// has 128 tokens.
+//
+// A block carries the state of one head through the chunks of one segment.  Per chunk:
+//   (1) G  = C B^T                      128 t x 128 s, K = 128
+//       M_ts = G_ts exp(l_t - l_s) delta_s, rounded to two bf16 planes in tensor memory
+//   (2) D1 = C S^T                      128 t x 64 p, K = 128, S as two bf16 planes
+//   (3) D2 = M X                        128 t x 64 p, K = 128, A operand M from tensor memory
+//       y_t = exp(l_t) D1_t + D2_t + D x_t
+//   (4) D3 = B^T (X delta exp(l_128 - l))   128 n x 64 p, K = 128, the scaled x as three planes
+//       S <- exp(l_128) S + D3, in fp32 registers (lane n, 64 rows p)
+// Only (2) waits for the state, and the state only for (4): G, M and (4) of the next
+// chunk run ahead of it.  The outputs round to bf16, so two planes (2^-18) do for M and
+// the S of (2); the state stays fp32 and takes three.  D3 starts from zero at every chunk
+// and is added in fp32: the tensor cores cut their sums, and a state that was their
+// accumulator would lose 2^-23 at every step of a long sequence.
+//
+// 24 warps, each on one job, in step through mbarriers:
+//   0-7   M from G (row t per lane; the 32 x 32 blocks of the lower triangle, shared by two warps)
+//   8-15  the state (lane n, half of p each), its planes, and y (lane t)
+//   16-19 the scaled x, in pieces of 32 tokens through a ring of two
+//   20    loads (TMA);   21 issues every product;   22, 23 the decays of every other chunk
+//         (a chunk's take them some 5000 cycles of dependent steps, hence two, and three
+//         chunks' room)
+// The tensor work is 2304 cycles a chunk: 512 + 512 + 512 + 768.
+#include <cuda.h>
+
+#include "scan_common.cuh"
+#include "tma_host.cuh"
+
+namespace wkv7 {
+namespace {
+
+constexpr int kL = 128;         // tokens per chunk
+constexpr int kN = 128;         // columns of the state
+constexpr int kWarpS = 8, kWarpX = 16, kWarpLoad = 20, kWarpMma = 21, kWarpDec = 22;
+constexpr int kTcThreads = 24 * 32;
+constexpr int kDecs = 3;  // chunks whose decays are kept
+constexpr int kHalf = kScanP / 2;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+constexpr uint32_t kTile = kL * 128;         // 128 rows of 128 bytes (64 bf16): one atom column
+constexpr uint32_t kStage = kTile + 4 * kTile;  // X, B (two atoms), C (two atoms)
+constexpr uint32_t kOffS = 2 * kStage;       // two planes of S^T: rows n, 64 p
+constexpr uint32_t kPiece = 32 * 128;        // 32 tokens of scaled x, one plane
+constexpr uint32_t kOffXw = kOffS + 2 * kTile;
+constexpr uint32_t kOffDec = kOffXw + 2 * 3 * kPiece;
+
+struct Decays128 {
+    float delta[kL], hi[kL], lo[kL];  // hi + lo = l_t log2(e)
+    float from[kL];                   // exp(l_t)
+    float w[kL];                      // delta_t exp(l_128 - l_t)
+    float total, pad[3];
+};
+constexpr uint32_t kOffBar = kOffDec + kDecs * sizeof(Decays128);
+struct Bars {
+    uint64_t full[2], empty[2], dec_full[kDecs], dec_empty[kDecs], xw_full[2], xw_empty[2], d3_full[2];
+    uint64_t g_full, m_full, s_full, d1_full, d2_full, d_empty, fin;
+    uint32_t tmem;
+};
+constexpr uint32_t kTcSmem = kOffBar + sizeof(Bars) + 1024;  // + alignment of the tiles
+static_assert(kTcSmem <= 227 * 1024, "shared memory of an SM");
+
+// tensor memory columns
+constexpr uint32_t kColG = 0, kColM = 128, kColD1 = 256, kColD2 = 320, kColD3 = 384;  // D3 twice
+
+constexpr uint32_t kIdG = idesc_f32acc(1, 128, 128, 0, 0);
+constexpr uint32_t kIdY = idesc_f32acc(1, 128, 64, 0, 1);   // A K-major (or tensor memory), B rows are K
+constexpr uint32_t kIdS = idesc_f32acc(1, 128, 64, 1, 1);   // both rows are K
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    const uint32_t z = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(z), "r"(z), "r"(z), "r"(z));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&f)[16]) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]),
+          "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&f)[8]) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(f[0]),
+        "r"(f[1]), "r"(f[2]), "r"(f[3]), "r"(f[4]), "r"(f[5]), "r"(f[6]), "r"(f[7]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptors of a tile: K-major (rows are M or N, two atom columns), or with K as rows and
+// `lbo` bytes between the atom columns.  The address field counts 16 bytes, so K-step k
+// (16 elements) is an addition of a constant: the one thread that issues the products has
+// no time to build descriptors.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return sdesc_sw128(addr, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) { return sdesc_sw128(addr, lbo, 1024); }
+__host__ __device__ constexpr uint64_t step_k(int k) { return (k >> 2) * (kTile >> 4) + (k & 3) * 2; }
+__host__ __device__ constexpr uint64_t step_mn(int k) { return k * 128; }
+__host__ __device__ constexpr uint64_t at(uint32_t bytes) { return bytes >> 4; }  // further on in shared memory
+
+struct TcMaps {
+    CUtensorMap x, b, c;
+};
+struct TcArgs {
+    const void* dt;
+    long lddt, ldy;
+    const float *A, *D, *bias, *s0;
+    __nv_bfloat16* y;
+    float *sT, *seg_state, *seg_decay;
+    int H, G, softplus, dt_bf16;
+    SegMap map;
+    int* status;
+};
+
+// Warp: the decays of a chunk from the raw dt of tokens 4 lane .. 4 lane + 3.
+__device__ __forceinline__ void chunk_decays128(Decays128& d, const float (&dt)[4], int n, float A, float bias,
+                                                bool softplus, int lane) {
+    constexpr double kLog2e = 1.4426950408889634074;
+    const double s = static_cast<double>(A) * kLog2e;
+    float e[4];
+    double l[4], run = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e[i] = dt[i] + bias;
+        if (softplus) e[i] = softplus_f32(e[i]);
+        if (4 * lane + i >= n) e[i] = 0.f;
+        run += e[i] * s;
+        l[i] = run;
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, run, m);
+        if (lane >= m) run += o;
+    }
+    double before = __shfl_up_sync(0xffffffffu, run, 1);
+    if (lane == 0) before = 0.0;
+    const double end = __shfl_sync(0xffffffffu, run, 31);
+    float hi[4], lo[4], from[4], w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const double c = before + l[i];
+        hi[i] = static_cast<float>(c);
+        lo[i] = static_cast<float>(c - hi[i]);
+        from[i] = exp2_f64(c);
+        w[i] = e[i] * exp2_f64(end - c);
+    }
+    *reinterpret_cast<float4*>(&d.delta[4 * lane]) = make_float4(e[0], e[1], e[2], e[3]);
+    *reinterpret_cast<float4*>(&d.hi[4 * lane]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<float4*>(&d.lo[4 * lane]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<float4*>(&d.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
+    *reinterpret_cast<float4*>(&d.w[4 * lane]) = make_float4(w[0], w[1], w[2], w[3]);
+    if (lane == 31) d.total = exp2_f64(end);
+}
+
+// OUT, whole: as in scan_kernel (wkv7_scan.cu).
+template <bool OUT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    scan_tc_kernel(const TcArgs a, bool whole, const __grid_constant__ TcMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    Bars& bar = *reinterpret_cast<Bars*>(sm + kOffBar);
+    Decays128* dec = reinterpret_cast<Decays128*>(sm + kOffDec);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % a.H, grp = h / (a.H / a.G);
+    const long slot = blockIdx.x / a.H;
+    constexpr long kState = static_cast<long>(kScanP) * kN;
+
+    int n;
+    long r0, r1, lo, hi;
+    if (!seg_rows(a.map, slot, n, r0, r1, lo, hi, a.status)) {
+        // an empty sequence passes its state on (its first slot does that)
+        if (!whole || !a.sT || hi > lo || slot != seg_first(a.map, n, lo)) return;
+        const long e = (static_cast<long>(n) * a.H + h) * kState;
+        for (int i = tid; i < kState; i += kTcThreads) a.sT[e + i] = a.s0 ? a.s0[e + i] : 0.f;
+        return;
+    }
+    const long seq_state = (static_cast<long>(n) * a.H + h) * kState;
+    const long slot_state = (slot * a.H + h) * kState;
+    const int rows = static_cast<int>(r1 - r0), chunks = (rows + kL - 1) / kL;
+    auto count = [&](int c) { return rows - c * kL < kL ? rows - c * kL : kL; };
+
+    if (warp == kWarpMma) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bar.full[i], 1);
+                mbar_init(&bar.empty[i], OUT ? 9 : 1);
+                mbar_init(&bar.xw_full[i], 4);
+                mbar_init(&bar.xw_empty[i], 1);
+                mbar_init(&bar.d3_full[i], 1);
+            }
+            for (int i = 0; i < kDecs; ++i) {
+                mbar_init(&bar.dec_full[i], 1);
+                mbar_init(&bar.dec_empty[i], OUT ? 20 : 12);
+            }
+            mbar_init(&bar.g_full, 1);
+            mbar_init(&bar.m_full, 8);
+            mbar_init(&bar.s_full, 8);
+            mbar_init(&bar.d1_full, 1);
+            mbar_init(&bar.d2_full, 1);
+            mbar_init(&bar.d_empty, 8);
+            mbar_init(&bar.fin, 1);
+            fence_mbar_init();
+        }
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = bar.tmem;
+    const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lanes 32 (warp % 4) ..
+    bool ok = true;
+    // Waits for phase number `k` (0, 1, ..) of a barrier, for a limited time: one lane polls,
+    // and the warp goes on or gives up as one.
+    auto wait = [&](uint64_t& b, int k) {
+        const bool done = !ok || lane != 0 || mbar_wait(&b, static_cast<uint32_t>(k) & 1u, kWaitNs);
+        ok = __all_sync(0xffffffffu, done) && ok;
+    };
+    auto signal = [&](uint64_t& b) {  // once per warp
+        __syncwarp();
+        if (lane == 0) arrive(&b);
+    };
+
+    if (warp < kWarpS) {
+        // ------------------------------------------------------------ M from G
+        if constexpr (OUT) {
+            const int q = warp & 3, half = warp >> 2;
+            const int t = 32 * q + lane;
+            const uint32_t tG = tm + lane_base + kColG, tM = tm + lane_base + kColM;
+            {  // the blocks above the diagonal are zero for good
+                const uint32_t z[8] = {};
+                for (int j = half; j < 4; j += 2)
+                    if (j > q)
+                        for (int i = 0; i < 16; i += 8) {
+                            tmem_store8(tM + 16 * j + i, z);
+                            tmem_store8(tM + 64 + 16 * j + i, z);
+                        }
+                tmem_store_wait();
+            }
+            for (int c = 0; c < chunks && ok; ++c) {
+                wait(bar.dec_full[c % kDecs], c / kDecs);
+                // G of this chunk comes after (3) of the last one on the tensor cores, so M is free too
+                wait(bar.g_full, c);
+                if (!ok) break;
+                tc_fence_after();
+                const Decays128& d = dec[c % kDecs];
+                const float ht = d.hi[t], lt = d.lo[t];
+                for (int j = half; j <= q; j += 2)
+#pragma unroll
+                    for (int b = 0; b < 32; b += 16) {
+                        float g[16];
+                        tmem_load16(tG + 32 * j + b, g);
+                        uint32_t p0[8], p1[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const int s = 32 * j + b + i;
+                            const float4 hs = *reinterpret_cast<const float4*>(&d.hi[s]);
+                            const float4 ls = *reinterpret_cast<const float4*>(&d.lo[s]);
+                            const float4 ds = *reinterpret_cast<const float4*>(&d.delta[s]);
+                            float m[4];
+                            m[0] = g[i] * (ex2_ftz((ht - hs.x) + (lt - ls.x)) * ds.x);
+                            m[1] = g[i + 1] * (ex2_ftz((ht - hs.y) + (lt - ls.y)) * ds.y);
+                            m[2] = g[i + 2] * (ex2_ftz((ht - hs.z) + (lt - ls.z)) * ds.z);
+                            m[3] = g[i + 3] * (ex2_ftz((ht - hs.w) + (lt - ls.w)) * ds.w);
+                            if (j == q) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) m[e] = s + e <= t ? m[e] : 0.f;
+                            }
+                            uint32_t u[2];
+                            split_pair<2>(u, m[0], m[1]);
+                            p0[i / 2] = u[0], p1[i / 2] = u[1];
+                            split_pair<2>(u, m[2], m[3]);
+                            p0[i / 2 + 1] = u[0], p1[i / 2 + 1] = u[1];
+                        }
+                        tmem_store8(tM + 16 * j + b / 2, p0);
+                        tmem_store8(tM + 64 + 16 * j + b / 2, p1);
+                    }
+                tmem_store_wait();
+                tc_fence_before();
+                signal(bar.m_full);
+                signal(bar.dec_empty[c % kDecs]);
+            }
+        }
+    } else if (warp < kWarpX) {
+        // ------------------------------------------------------------ the state and y
+        const int row = 32 * (warp & 3) + lane;       // column n of the state; token t of y
+        const int p0 = warp >= kWarpS + 4 ? kHalf : 0;  // this warp's rows p of the state and channels of y
+        float S[kHalf];
+        {
+            const float* src = whole ? (a.s0 ? a.s0 + seq_state : nullptr) : OUT ? a.seg_state + slot_state : nullptr;
+#pragma unroll
+            for (int p = 0; p < kHalf; ++p) S[p] = src ? src[(p0 + p) * kN + row] : 0.f;
+        }
+        auto write_planes = [&]() {  // S^T: row n, 64 p, swizzled, for (2)
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 8) {
+                uint32_t u[4][2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_pair<2>(u[e], S[i + 2 * e], S[i + 2 * e + 1]);
+                const uint32_t o = swz(row, (p0 + i) * 2, kN);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    *reinterpret_cast<uint4*>(sm + kOffS + p * kTile + o) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
+            }
+            fence_proxy_async_smem();
+            signal(bar.s_full);
+        };
+        if constexpr (OUT) write_planes();
+        const float Dh = OUT && a.D ? a.D[h] : 0.f;
+        float run = 1.f;
+        for (int c = 0; c < chunks && ok; ++c) {
+            const Decays128& d = dec[c % kDecs];
+            wait(bar.dec_full[c % kDecs], c / kDecs);
+            wait(bar.d3_full[c & 1], c >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            const float tot = d.total, f = d.from[row];
+            signal(bar.dec_empty[c % kDecs]);
+            run *= tot;
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 16) {
+                float v[16];
+                tmem_load16(tm + lane_base + kColD3 + 64 * (c & 1) + p0 + i, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[i + e] = fmaf(tot, S[i + e], v[e]);
+            }
+            tc_fence_before();
+            if constexpr (OUT) {
+                wait(bar.d1_full, c);  // (2) has read the planes
+                if (!ok) break;
+                if (c + 1 < chunks) write_planes();
+                wait(bar.d2_full, c);
+                if (!ok) break;
+                tc_fence_after();
+                const uint8_t* xs = sm + (c & 1) * kStage;
+                __nv_bfloat16* dst = a.y + (r0 + static_cast<long>(c) * kL + row) * a.ldy + h * kScanP + p0;
+                const bool live = row < count(c);
+#pragma unroll
+                for (int i = 0; i < kHalf; i += 16) {
+                    float u[16], v[16];
+                    tmem_load16(tm + lane_base + kColD1 + p0 + i, u);
+                    tmem_load16(tm + lane_base + kColD2 + p0 + i, v);
+                    if (i == kHalf - 16) {
+                        tc_fence_before();
+                        signal(bar.d_empty);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; k += 8) {
+                        const uint4 xv = *reinterpret_cast<const uint4*>(xs + swz(row, (p0 + i + k) * 2, kL));
+                        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = pack_bf16(fmaf(Dh, bf_lo(xw[e]), fmaf(f, u[k + 2 * e], v[k + 2 * e])),
+                                             fmaf(Dh, bf_hi(xw[e]), fmaf(f, u[k + 2 * e + 1], v[k + 2 * e + 1])));
+                        if (live) *reinterpret_cast<uint4*>(dst + i + k) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                signal(bar.empty[c & 1]);
+            }
+        }
+        float* dst = whole ? (a.sT ? a.sT + seq_state : nullptr) : OUT ? nullptr : a.seg_state + slot_state;
+        if (ok && dst) {
+#pragma unroll
+            for (int p = 0; p < kHalf; ++p) dst[(p0 + p) * kN + row] = S[p];
+        }
+        if (!OUT && !whole && warp == kWarpS && lane == 0) a.seg_decay[slot * a.H + h] = run;
+    } else if (warp < kWarpLoad) {
+        // ------------------------------------------------------------ the scaled x
+        const int w = tid - kWarpX * 32, r = w >> 2, part = (w & 3) * 32;  // row of a piece; bytes part .. of it
+        for (int c = 0; c < chunks && ok; ++c) {
+            const Decays128& d = dec[c % kDecs];
+            const int nr = count(c);
+            uint8_t* st = sm + (c & 1) * kStage;
+            wait(bar.full[c & 1], c >> 1);
+            wait(bar.dec_full[c % kDecs], c / kDecs);
+            for (int k = 0; k < 4 && ok; ++k) {
+                const int piece = 4 * c + k, s = 32 * k + r;
+                if (piece >= 2) wait(bar.xw_empty[piece & 1], (piece >> 1) - 1);
+                if (!ok) break;
+                const bool live = s < nr;
+                const float f = d.w[s];
+                uint8_t* out = sm + kOffXw + (piece & 1) * 3 * kPiece;
+#pragma unroll
+                for (int b = 0; b < 32; b += 16) {
+                    const uint4 xv = *reinterpret_cast<const uint4*>(st + swz(s, part + b, kL));
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    uint32_t u[4][3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        split_pair<3>(u[e], live ? f * bf_lo(xw[e]) : 0.f, live ? f * bf_hi(xw[e]) : 0.f);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<uint4*>(out + p * kPiece + swz(r, part + b, 32)) =
+                            make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
+                    if (!live) {
+                        // Rows of the next sequence: their x and B meet factors of zero in (3) and (4),
+                        // which an infinity or NaN would not survive.
+                        const uint4 z = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(st + swz(s, part + b, kL)) = z;
+                        *reinterpret_cast<uint4*>(st + kTile + swz(s, part + b, kL)) = z;
+                        *reinterpret_cast<uint4*>(st + 2 * kTile + swz(s, part + b, kL)) = z;
+                    }
+                }
+                fence_proxy_async_smem();
+                signal(bar.xw_full[piece & 1]);
+            }
+            signal(bar.dec_empty[c % kDecs]);
+        }
+    } else if (warp == kWarpLoad) {
+        // ------------------------------------------------------------ loads
+        int issued = 0;
+        for (int c = 0; c < chunks && ok; ++c) {
+            const int st = c & 1;
+            if (c >= 2) wait(bar.empty[st], (c >> 1) - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                uint8_t* p = sm + st * kStage;
+                const int row = static_cast<int>(r0 + static_cast<long>(c) * kL);
+                mbar_arrive_expect_tx(&bar.full[st], OUT ? kStage : 3 * kTile);
+                tma_load_2d(p + kTile, &maps.b, &bar.full[st], grp * kN, row);
+                tma_load_2d(p + 2 * kTile, &maps.b, &bar.full[st], grp * kN + 64, row);
+                if constexpr (OUT) {
+                    tma_load_2d(p + 3 * kTile, &maps.c, &bar.full[st], grp * kN, row);
+                    tma_load_2d(p + 4 * kTile, &maps.c, &bar.full[st], grp * kN + 64, row);
+                }
+                tma_load_2d(p, &maps.x, &bar.full[st], h * kScanP, row);
+            }
+            __syncwarp();
+            issued = c + 1;
+        }
+        // nothing may still be on its way into shared memory when the block ends
+        if (!ok)
+            for (int c = issued < 2 ? 0 : issued - 2; c < issued; ++c)
+                mbar_wait(&bar.full[c & 1], static_cast<uint32_t>(c >> 1) & 1u, kWaitNs);
+    } else if (warp >= kWarpDec) {
+        // ------------------------------------------------------------ decays
+        const float Ah = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
+        float dt[4];
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long r = r0 + static_cast<long>(c) * kL + 4 * lane + i;
+                dt[i] = r < r1 ? load_dt(a.dt, r * a.lddt + h, a.dt_bf16) : 0.f;
+            }
+        };
+        fetch(warp - kWarpDec);
+        for (int c = warp - kWarpDec; c < chunks && ok; c += 2) {
+            if (c >= kDecs) wait(bar.dec_empty[c % kDecs], c / kDecs - 1);
+            if (!ok) break;
+            chunk_decays128(dec[c % kDecs], dt, count(c), Ah, bias, a.softplus, lane);
+            fetch(c + 2);
+            signal(bar.dec_full[c % kDecs]);
+        }
+    } else if (lane == 0) {
+        // ------------------------------------------------------------ products
+        auto wait1 = [&](uint64_t& b, int k) { ok = ok && mbar_wait(&b, static_cast<uint32_t>(k) & 1u, kWaitNs); };
+        const uint64_t dX = desc_mn(sb, kTile), dBk = desc_k(sb + kTile), dBn = desc_mn(sb + kTile, kTile),
+                       dC = desc_k(sb + 3 * kTile), dS = desc_mn(sb + kOffS, kTile), dXw = desc_mn(sb + kOffXw, kPiece);
+        auto products_g = [&](int c) {
+            const uint64_t st = (c & 1) * at(kStage);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_ss<false>(tm + kColG, dC + st + step_k(k), dBk + st + step_k(k), kIdG, k > 0);
+            mma_commit(&bar.g_full);
+        };
+        for (int c = 0; c < chunks && ok; ++c) {
+            const int st = c & 1;
+            const uint64_t so = st * at(kStage);
+            if (!OUT || c == 0) {
+                wait1(bar.full[st], c >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (OUT) products_g(0);
+            }
+            // (4)
+            const uint32_t d3 = tm + kColD3 + 64 * st;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int piece = 4 * c + k;
+                wait1(bar.xw_full[k & 1], piece >> 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mma_ss<false>(d3, dBn + so + step_mn(2 * k + j),
+                                      dXw + at((k & 1) * 3 * kPiece + p * kPiece) + step_mn(j), kIdS,
+                                      k > 0 || p > 0 || j > 0);
+                mma_commit(&bar.xw_empty[k & 1]);
+            }
+            if (!ok) break;
+            mma_commit(&bar.d3_full[st]);
+            if constexpr (!OUT) {
+                mma_commit(&bar.empty[st]);
+            } else {
+                // (2)
+                wait1(bar.s_full, c);
+                if (c > 0) wait1(bar.d_empty, c - 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ss<false>(tm + kColD1, dC + so + step_k(k), dS + at(p * kTile) + step_mn(k), kIdY,
+                                      p > 0 || k > 0);
+                mma_commit(&bar.d1_full);
+                // (3)
+                wait1(bar.m_full, c);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(tm + kColD2, tm + kColM + 64 * p + 8 * k, dX + so + step_mn(k), kIdY, p > 0 || k > 0);
+                mma_commit(&bar.d2_full);
+                mma_commit(&bar.empty[st]);
+                // (1) of the next chunk: M of this one has been made, so G is free
+                if (c + 1 < chunks) {
+                    wait1(bar.full[st ^ 1], (c + 1) >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    products_g(c + 1);
+                }
+            }
+        }
+        // every product is complete before tensor memory is given back
+        mma_commit(&bar.fin);
+        ok = mbar_wait(&bar.fin, 0, kWaitNs) && ok;
+    }
+    __syncwarp();
+    if (!ok && lane == 0) report_status(a.status, WKV7_ERR_DEVICE_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// rows x width matrix of bf16 at a row stride, box 64 columns x 128 rows
+bool make_map(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint64_t ld) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {width, rows};
+    const cuuint64_t strides[1] = {ld * 2};
+    const cuuint32_t box[2] = {64, kL};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_scan_tc(const ScanArgs& p, const SegMap& map, bool whole, bool out, float* seg_state,
+                           float* seg_decay, cudaStream_t stream) {
+    TcMaps maps;
+    const uint64_t rows = p.seq_offsets ? p.T : static_cast<uint64_t>(p.B) * p.T;
+    if (!make_map(&maps.x, p.x, static_cast<uint64_t>(p.H) * kScanP, rows, p.ldx) ||
+        !make_map(&maps.b, p.Bm, static_cast<uint64_t>(p.G) * kN, rows, p.ldb) ||
+        !make_map(&maps.c, p.Cm, static_cast<uint64_t>(p.G) * kN, rows, p.ldc))
+        return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> cfg_out{0}, cfg_state{0};
+    const TcArgs a{p.dt, p.lddt, p.ldy, p.A, p.D, p.dt_bias, p.s0, static_cast<__nv_bfloat16*>(p.y), p.sT, seg_state,
+                   seg_decay, p.H, p.G, p.softplus, p.dt_dtype == WKV7_BF16, map, p.status};
+    const unsigned grid = static_cast<unsigned>(seg_slots(map) * p.H);
+    cudaError_t e;
+    if (out) {
+        e = configure_smem_once(scan_tc_kernel<true>, kTcSmem, cfg_out);
+        if (e == cudaSuccess) scan_tc_kernel<true><<<grid, kTcThreads, kTcSmem, stream>>>(a, whole, maps);
+    } else {
+        e = configure_smem_once(scan_tc_kernel<false>, kTcSmem, cfg_state);
+        if (e == cudaSuccess) scan_tc_kernel<false><<<grid, kTcThreads, kTcSmem, stream>>>(a, whole, maps);
+    }
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace wkv7
