@@ -389,7 +389,7 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
  *   s0 : [B][H][64][N] fp32 or NULL (zeros);  sT : the same shape or NULL; sT == s0 is
  *   allowed.  T == 0: sT receives s0.
  *   workspace : at least wkv7_selective_scan_workspace_bytes(B, T, H, D, N, packed)
- *   bytes, which is 0 (workspace may be NULL) when sequences and heads fill the GPU.
+ *   bytes.  (0, and workspace may then be NULL, for T == 0.)
  * D must be 64, N one of 16, 32, 64 and 128, G a divisor of H.  x, Bm, Cm and y need
  * row strides of a multiple of 16 bytes; dt only the alignment of its elements.
  * A dt of -inf leaves the state as it is (padding): x, Bm and Cm of such a token must

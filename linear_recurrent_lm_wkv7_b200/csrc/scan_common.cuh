@@ -137,6 +137,29 @@ __device__ __forceinline__ void chunk_decays(Decays& d, float dt0, float dt1, in
     if (lane == 31) d.total = exp2_f64(end);
 }
 
+// The decays of every (chunk slot, head) of `map` (segments of one chunk): out [slot][H].
+// Made once, by a warp each: a chunk's take thousands of cycles of dependent steps
+// (softplus, a scan in 64 bits), which in the kernels that walk chunks one after the
+// other would stand in the way of every chunk@@MEAS@@.
+struct DecayArgs {
+    const void* dt;
+    long lddt;
+    const float *A, *bias;
+    Decays* out;
+    int H, softplus, dt_bf16;
+    SegMap map;
+    int* status;
+};
+cudaError_t launch_decays(const DecayArgs& a, cudaStream_t stream);
+// The cut at every chunk, and how many slots it has at most.
+SegMap chunk_map(int B, int T, const int32_t* offs);
+long chunk_slots(int B, int T, bool packed);
+static_assert(sizeof(Decays) % 16 == 0, "copied in 16-byte pieces");
+__device__ __forceinline__ void cp_decays(uint32_t dst, const Decays* src, int tid) {
+    if (tid < static_cast<int>(sizeof(Decays) / 16))
+        cp_async16(dst + tid * 16, reinterpret_cast<const uint8_t*>(src) + tid * 16, true);
+}
+
 // ---------------------------------------------------------------- tile loads
 // Rows [0, 64) x COLS of a chunk into a tile: row r from src + r * ld while r < n,
 // zeros behind.  bf16: asynchronous copies.  fp32: split into planes on the way.
@@ -155,19 +178,38 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
-template <typename TL, int COLS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const float* src, long ld, int n, int tid, int threads) {
-    constexpr int per = COLS / 4;
-    for (int i = tid; i < kChunk * per; i += threads) {
-        const int r = i / per, c = i % per;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) v = *reinterpret_cast<const float4*>(src + r * ld + c * 4);
-        uint32_t a[TL::planes], b[TL::planes];
-        split_pair<TL::planes>(a, v.x, v.y);
-        split_pair<TL::planes>(b, v.z, v.w);
+// fp32 rows on their way through registers: all of a tile's loads are in flight before
+// the first is split (one latency a tile, not one an access).
+template <int COLS, int THREADS>
+struct TileRegs {
+    static constexpr int per = COLS / 4, count = kChunk * per / THREADS;
+    static_assert(kChunk * per % THREADS == 0, "whole turns");
+    float4 v[count];
+    __device__ __forceinline__ void fetch(const float* src, long ld, int n, int tid) {
 #pragma unroll
-        for (int p = 0; p < TL::planes; ++p) sts64(dst + p * TL::plane + r * TL::pitch + c * 8, a[p], b[p]);
+        for (int k = 0; k < count; ++k) {
+            const int i = tid + k * THREADS, r = i / per, c = i % per;
+            v[k] = r < n ? *reinterpret_cast<const float4*>(src + r * ld + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
+    template <typename TL>
+    __device__ __forceinline__ void put(uint32_t dst, int tid) const {
+#pragma unroll
+        for (int k = 0; k < count; ++k) {
+            const int i = tid + k * THREADS, r = i / per, c = i % per;
+            uint32_t a[TL::planes], b[TL::planes];
+            split_pair<TL::planes>(a, v[k].x, v[k].y);
+            split_pair<TL::planes>(b, v[k].z, v[k].w);
+#pragma unroll
+            for (int p = 0; p < TL::planes; ++p) sts64(dst + p * TL::plane + r * TL::pitch + c * 8, a[p], b[p]);
+        }
+    }
+};
+template <typename TL, int COLS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const float* src, long ld, int n, int tid, int) {
+    TileRegs<COLS, kScanThreads> t;
+    t.fetch(src, ld, n, tid);
+    t.template put<TL>(dst, tid);
 }
 
 __device__ __forceinline__ float load_dt(const void* dt, long i, bool bf16) {

@@ -144,7 +144,8 @@ struct ScanArgs {
     const float *D, *dt_bias, *s0;
     void* y;
     long ldy;
-    float *sT, *ws;
+    float* sT;
+    void* ws;
     int B, T, H, N, G;
     const int32_t* seq_offsets;
     int softplus, dt_dtype;

@@ -15,6 +15,8 @@
 // segments: a first pass takes every segment's state from zero, a join walks the
 // segments of a head (S <- decay S + segment's state), and a second pass starts each
 // segment from its true state.
+#include <type_traits>
+
 #include "scan_common.cuh"
 
 namespace wkv7 {
@@ -44,15 +46,30 @@ struct FwdLayout {
     static constexpr int bytes = off_d + 2 * static_cast<int>(sizeof(Decays));
 };
 
+__global__ void __launch_bounds__(256) decays_kernel(const DecayArgs a) {
+    const long u = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (u >= seg_slots(a.map) * a.H) return;
+    const long slot = u / a.H;
+    const int h = static_cast<int>(u % a.H);
+    int n;
+    long r0, r1, lo, hi;
+    if (!seg_rows(a.map, slot, n, r0, r1, lo, hi, a.status)) return;
+    const long r = r0 + 2 * lane;
+    const float dt0 = r < r1 ? load_dt(a.dt, r * a.lddt + h, a.dt_bf16) : 0.f;
+    const float dt1 = r + 1 < r1 ? load_dt(a.dt, (r + 1) * a.lddt + h, a.dt_bf16) : 0.f;
+    chunk_decays(a.out[u], dt0, dt1, static_cast<int>(r1 - r0), a.A[h], a.bias ? a.bias[h] : 0.f, a.softplus, lane);
+}
+
 struct ScanDev {
-    const void *x, *dt, *Bm, *Cm;
-    long ldx, lddt, ldb, ldc, ldy;
-    const float *A, *D, *bias, *s0;
+    const void *x, *Bm, *Cm;
+    long ldx, ldb, ldc, ldy;
+    const float *D, *s0;
     void* y;
     float *sT, *seg_state, *seg_decay;
     int H, G;
-    int softplus, dt_bf16;
-    SegMap map;
+    SegMap map, chunk;  // segments, and the same cut at 64 tokens
+    const Decays* dec;  // [chunk][H]
     int* status;
 };
 
@@ -99,37 +116,43 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
     const IO* cg = static_cast<const IO*>(a.Cm) + r0 * a.ldc + static_cast<long>(grp) * N;
     const int rows = static_cast<int>(r1 - r0);
     const int chunks = (rows + kChunk - 1) / kChunk;
-    const float Ah = a.A[h], bias = a.bias ? a.bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    const float Dh = a.D ? a.D[h] : 0.f;
+    const Decays* dg = a.dec + (seg_first(a.chunk, n, lo) + (r0 - lo) / kChunk) * a.H + h;
 
     auto stage = [&](int c) { return sb + (c % LY::stages) * LY::stage_bytes; };
+    auto count = [&](int c) { return rows - c * kChunk < kChunk ? rows - c * kChunk : kChunk; };
     auto load = [&](int c) {
-        const int left = rows - c * kChunk, nr = left < kChunk ? left : kChunk;
+        const int nr = count(c);
         const uint32_t s = stage(c);
         load_tile<TX, kScanP>(s, xg + static_cast<long>(c) * kChunk * a.ldx, a.ldx, nr, tid, kScanThreads);
         load_tile<TB, N>(s + TX::bytes, bg + static_cast<long>(c) * kChunk * a.ldb, a.ldb, nr, tid, kScanThreads);
         if constexpr (OUT)
             load_tile<TB, N>(s + TX::bytes + TB::bytes, cg + static_cast<long>(c) * kChunk * a.ldc, a.ldc, nr, tid,
                              kScanThreads);
-        if constexpr (LY::stages == 2) cp_async_commit();
     };
-    // raw dt of chunk c, tokens 2 lane and 2 lane + 1 (warp 0)
-    float dt0 = 0.f, dt1 = 0.f;
-    auto fetch_dt = [&](int c) {
-        const long r = r0 + static_cast<long>(c) * kChunk + 2 * lane;
-        dt0 = r < r1 ? load_dt(a.dt, r * a.lddt + h, a.dt_bf16) : 0.f;
-        dt1 = r + 1 < r1 ? load_dt(a.dt, (r + 1) * a.lddt + h, a.dt_bf16) : 0.f;
+    auto load_decays = [&](int c) {
+        cp_decays(sb + LY::off_d + (c & 1) * static_cast<uint32_t>(sizeof(Decays)), dg + static_cast<long>(c) * a.H, tid);
+        cp_async_commit();
     };
-    auto make_decays = [&](int c) {
-        const int left = rows - c * kChunk;
-        chunk_decays(dec[c & 1], dt0, dt1, left < kChunk ? left : kChunk, Ah, bias, a.softplus, lane);
+    // fp32: the next chunk's rows in registers, where they fit (N <= 64)
+    constexpr bool kAhead = LY::stages == 1 && N <= 64;
+    struct Next {
+        TileRegs<kScanP, kScanThreads> x;
+        TileRegs<N, kScanThreads> b, c;
     };
-
+    struct None {};
+    std::conditional_t<kAhead, Next, None> nx;
+    auto fetch = [&](int c) {
+        if constexpr (kAhead) {
+            const int nr = count(c);
+            nx.x.fetch(xg + static_cast<long>(c) * kChunk * a.ldx, a.ldx, nr, tid);
+            nx.b.fetch(bg + static_cast<long>(c) * kChunk * a.ldb, a.ldb, nr, tid);
+            if constexpr (OUT) nx.c.fetch(cg + static_cast<long>(c) * kChunk * a.ldc, a.ldc, nr, tid);
+        }
+    };
     if constexpr (LY::stages == 2) load(0);
-    if (warp == 0) {
-        fetch_dt(0);
-        make_decays(0);
-        if (chunks > 1) fetch_dt(1);
-    }
+    load_decays(0);
+    fetch(0);
 
     // state: S[i] = tile of columns n0 + 8 i; rows 16 pg + g8 (0, 1) and + 8 (2, 3)
     float S[NT][4];
@@ -156,11 +179,25 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
         if constexpr (LY::stages == 2) {
             cp_async_wait<0>();
             __syncthreads();
-            if (c + 1 < chunks) load(c + 1);
+            if (c + 1 < chunks) {
+                load(c + 1);
+                load_decays(c + 1);
+            }
         } else {
             __syncthreads();  // the last chunk's readers are done
-            load(c);
+            if constexpr (kAhead) {
+                nx.x.template put<TX>(stage(c), tid);
+                nx.b.template put<TB>(stage(c) + TX::bytes, tid);
+                if constexpr (OUT) nx.c.template put<TB>(stage(c) + TX::bytes + TB::bytes, tid);
+            } else {
+                load(c);
+            }
+            cp_async_wait<0>();
             __syncthreads();
+            if (c + 1 < chunks) {
+                load_decays(c + 1);
+                fetch(c + 1);
+            }
         }
         const Decays& d = dec[c & 1];
         const uint32_t sx = stage(c), sB = sx + TX::bytes, sC = sB + TB::bytes, sM = sb + LY::off_m;
@@ -251,10 +288,6 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
                     mma_planes<kStatePlanes, PI>(S[i + 1], fa, fb[1]);
                 }
             }
-        }
-        if (warp == 0 && c + 1 < chunks) {  // the next chunk's decays; read after the next barrier
-            make_decays(c + 1);
-            if (c + 2 < chunks) fetch_dt(c + 2);
         }
         if constexpr (OUT) {
             __syncthreads();  // M is complete
@@ -491,38 +524,60 @@ SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed, cons
     return m;
 }
 
-static size_t cut_bytes(int B, int T, int H, int N, bool packed, const CutCost& cost) {
+cudaError_t launch_decays(const DecayArgs& a, cudaStream_t stream) {
+    const long warps = seg_slots(a.map) * a.H;
+    if (warps > 0) decays_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+SegMap chunk_map(int B, int T, const int32_t* offs) { return SegMap{offs, B, T, kChunk, (T + kChunk - 1) / kChunk}; }
+long chunk_slots(int B, int T, bool packed) {
+    return packed ? T / kChunk + B : static_cast<long>(B) * ((static_cast<long>(T) + kChunk - 1) / kChunk);
+}
+
+// The segments' states and decays of either kernel (the size query does not know the io
+// type), and the chunks' decays of this file's.
+static size_t cut_floats(int B, int T, int H, int N, bool packed, const CutCost& cost) {
     const SegMap m = scan_segments(B, T, H, nullptr, packed, cost);
     if (m.seg >= T) return 0;
     const long slots = packed ? T / m.seg + B : static_cast<long>(B) * m.spb;
-    return static_cast<size_t>(slots) * H * (static_cast<size_t>(kScanP) * N + 4) * sizeof(float);
+    return static_cast<size_t>(slots) * H * (static_cast<size_t>(kScanP) * N + 4);
 }
-
-// Of either kernel: the size query does not know the io type.
+static size_t decays_bytes(int B, int T, int H, bool packed) {
+    return static_cast<size_t>(chunk_slots(B, T, packed)) * H * sizeof(Decays);
+}
 size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
-    const size_t w = cut_bytes(B, T, H, N, packed, kCutWarp);
-    const size_t t = N == 128 ? cut_bytes(B, T, H, N, packed, kCutTc) : 0;
+    const size_t w = cut_floats(B, T, H, N, packed, kCutWarp) * sizeof(float) + decays_bytes(B, T, H, packed);
+    const size_t t = N == 128 ? cut_floats(B, T, H, N, packed, kCutTc) * sizeof(float) : 0;
     return w > t ? w : t;
 }
 
 cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
-    const bool tc = uses_tc(io_dtype, p.N, p.seq_offsets ? p.T : static_cast<long>(p.B) * p.T);
-    const SegMap map =
-        scan_segments(p.B, p.T, p.H, p.seq_offsets, p.seq_offsets != nullptr, tc ? kCutTc : kCutWarp);
+    const bool packed = p.seq_offsets != nullptr;
+    const bool tc = uses_tc(io_dtype, p.N, packed ? p.T : static_cast<long>(p.B) * p.T);
+    const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, packed, tc ? kCutTc : kCutWarp);
     const bool whole = map.seg >= p.T;
-    ScanDev d{p.x, p.dt, p.Bm, p.Cm, p.ldx, p.lddt, p.ldb, p.ldc, p.ldy, p.A, p.D, p.dt_bias, p.s0, p.y, p.sT,
-              p.ws, whole ? nullptr : p.ws + static_cast<size_t>(seg_slots(map)) * p.H * kScanP * p.N, p.H, p.G,
-              p.softplus, p.dt_dtype == WKV7_BF16, map, p.status};
+    uint8_t* ws = static_cast<uint8_t*>(p.ws);
+    Decays* dec = reinterpret_cast<Decays*>(ws);
+    if (!tc) ws += decays_bytes(p.B, p.T, p.H, packed);
+    float* seg_state = reinterpret_cast<float*>(ws);
+    float* seg_decay = whole ? nullptr : seg_state + static_cast<size_t>(seg_slots(map)) * p.H * kScanP * p.N;
+    ScanDev d{p.x, p.Bm, p.Cm, p.ldx, p.ldb, p.ldc, p.ldy, p.D, p.s0, p.y, p.sT, seg_state, seg_decay, p.H, p.G,
+              map, chunk_map(p.B, p.T, p.seq_offsets), dec, p.status};
     if (tc) {
         cudaError_t e = cudaSuccess;
         if (!whole) {
-            e = launch_scan_tc(p, map, false, false, d.seg_state, d.seg_decay, stream);
+            e = launch_scan_tc(p, map, false, false, seg_state, seg_decay, stream);
             if (e != cudaSuccess) return e;
             constexpr int elems = kScanP * 128;
             scan_join_kernel<<<dim3(static_cast<unsigned>(p.B) * p.H, elems / 4 / 256), 256, 0, stream>>>(d, elems);
         }
-        return launch_scan_tc(p, map, whole, true, d.seg_state, d.seg_decay, stream);
+        return launch_scan_tc(p, map, whole, true, seg_state, seg_decay, stream);
     }
+    const cudaError_t e = launch_decays(DecayArgs{p.dt, p.lddt, p.A, p.dt_bias, dec, p.H, p.softplus,
+                                                  p.dt_dtype == WKV7_BF16, d.chunk, p.status},
+                                        stream);
+    if (e != cudaSuccess) return e;
     if (io_dtype == WKV7_BF16) switch (p.N) {
             case 16: return scan_typed<__nv_bfloat16, 16>(p, map, whole, d, stream);
             case 32: return scan_typed<__nv_bfloat16, 32>(p, map, whole, d, stream);

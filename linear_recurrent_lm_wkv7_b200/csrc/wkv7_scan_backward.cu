@@ -16,7 +16,7 @@
 // tokens that act on each other.  Last, d delta_s has the term
 // x_s . (sum G L dy + e dS B_s), and d softplus(u) / du = 1 - exp(-softplus(u)).
 //
-// Launches: (1) the states S_0 and the gradients dS at every chunk boundary, forwards
+// Launches: the decays; (1) the states S_0 and the gradients dS at every chunk boundary, forwards
 // and backwards side by side, written as bf16 planes (over segments where sequences
 // and heads are few, as in wkv7_scan.cu); (2) one block per chunk, group and share of
 // the group's heads, which keeps the sums over heads in registers: warps 0-3 hold 16
@@ -28,9 +28,9 @@ namespace wkv7 {
 namespace {
 
 struct BwdDev {
-    const void *x, *dt, *Bm, *Cm, *dy;
-    long ldx, lddt, ldb, ldc, lddy;
-    const float *A, *D, *bias, *s0, *dsT;
+    const void *x, *Bm, *Cm, *dy;
+    long ldx, ldb, ldc, lddy;
+    const float *A, *D, *s0, *dsT;
     void *dx, *ddt, *dB, *dC;
     long lddx, ldddt, lddb, lddc;
     float *dA, *dD, *dbias, *ds0;
@@ -38,6 +38,7 @@ struct BwdDev {
     SegMap seg, chunk;   // segments, and the same cut at 64 tokens
     long seg_count, chunk_count;
     // workspace
+    const Decays* dec;      // [chunk][H]
     __nv_bfloat16* states;  // [2][chunk][H][plane][64][N]: S_0 and dS
     float* seg_state;       // [2][seg][H][64][N]
     float* seg_decay;       // [seg][H]
@@ -56,7 +57,11 @@ struct StateLayout {
     static constexpr int stages = sizeof(IO) == 2 ? 2 : 1;
     static constexpr int stage_bytes = TX::bytes + TB::bytes;
     static constexpr int off_d = stages * stage_bytes;
-    static constexpr int bytes = off_d + 2 * static_cast<int>(sizeof(Decays));
+    // a warp's 16 rows of one plane of the state, for its way out in whole rows
+    static constexpr int cols = N / 2 >= 16 ? N / 2 : 16;
+    using TO = Tile<1, 16, cols>;
+    static constexpr int off_o = off_d + 2 * static_cast<int>(sizeof(Decays));
+    static constexpr int bytes = off_o + 8 * TO::bytes;
 };
 
 // blockIdx.y: 0 the states from x and B, forwards; 1 their gradients from dy and C,
@@ -98,7 +103,8 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
     xg += r0 * ldx + h * kScanP;
     bg += r0 * ldb + static_cast<long>(grp) * N;
     const int rows = static_cast<int>(r1 - r0), chunks = (rows + kChunk - 1) / kChunk;
-    const float Ah = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
+    const long chunk0 = seg_first(a.chunk, n, lo) + (r0 - lo) / kChunk;
+    const Decays* dg = a.dec + chunk0 * a.H + h;
 
     // i-th chunk of the walk
     auto at = [&](int i) { return back ? chunks - 1 - i : i; };
@@ -108,23 +114,10 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
         const int c = at(i), nr = count(c);
         load_tile<TX, kScanP>(stage(i), xg + static_cast<long>(c) * kChunk * ldx, ldx, nr, tid, kScanThreads);
         load_tile<TB, N>(stage(i) + TX::bytes, bg + static_cast<long>(c) * kChunk * ldb, ldb, nr, tid, kScanThreads);
-        if constexpr (LY::stages == 2) cp_async_commit();
-    };
-    float dt0 = 0.f, dt1 = 0.f;
-    auto fetch_dt = [&](int i) {
-        const long r = r0 + static_cast<long>(at(i)) * kChunk + 2 * lane;
-        dt0 = r < r1 ? load_dt(a.dt, r * a.lddt + h, a.dt_bf16) : 0.f;
-        dt1 = r + 1 < r1 ? load_dt(a.dt, (r + 1) * a.lddt + h, a.dt_bf16) : 0.f;
-    };
-    auto make_decays = [&](int i) {
-        chunk_decays(dec[i & 1], dt0, dt1, count(at(i)), Ah, bias, a.softplus, lane);
+        cp_decays(sb + LY::off_d + (i & 1) * static_cast<uint32_t>(sizeof(Decays)), dg + static_cast<long>(c) * a.H, tid);
+        cp_async_commit();
     };
     if constexpr (LY::stages == 2) load(0);
-    if (warp == 0) {
-        fetch_dt(0);
-        make_decays(0);
-        if (chunks > 1) fetch_dt(1);
-    }
     float S[NT][4];
     {
         const float* src = nullptr;
@@ -146,7 +139,6 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
         }
     }
     float run = 1.f;
-    const long chunk0 = seg_first(a.chunk, n, lo) + (r0 - lo) / kChunk;
     for (int i = 0; i < chunks; ++i) {
         if constexpr (LY::stages == 2) {
             cp_async_wait<0>();
@@ -155,23 +147,50 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
         } else {
             __syncthreads();
             load(i);
+            cp_async_wait<0>();
             __syncthreads();
         }
         const Decays& d = dec[i & 1];
         if (WRITE && has_n) {
             __nv_bfloat16* dst =
                 a.states + (((back ? a.chunk_count : 0) + chunk0 + at(i)) * a.H + h) * (PC * kState);
+            // Plane by plane through shared memory: rows of NH columns in 16-byte pieces
+            // (stored from the fragments, 4 bytes a lane, they took 71 % of the L1's time).
+            using TO = typename LY::TO;
+            const uint32_t so = sb + LY::off_o + warp * TO::bytes;
+            float rest[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    uint32_t u[PC];
-                    split_pair<PC>(u, S[j][2 * r], S[j][2 * r + 1]);
+                for (int e = 0; e < 4; ++e) rest[j][e] = S[j][e];
 #pragma unroll
-                    for (int p = 0; p < PC; ++p)
-                        *reinterpret_cast<uint32_t*>(dst + p * kState + (pg * 16 + g8 + 8 * r) * N + n0 + j * 8 + q2) =
-                            u[p];
+            for (int p = 0; p < PC; ++p) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t u[4];  // (rows 0-7, tile j) (rows 8-15, tile j) (0-7, j + 1) (8-15, j + 1)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float* v = &rest[j + (k >> 1)][2 * (k & 1)];
+                        u[k] = pack_bf16(v[0], v[1]);
+                        v[0] -= bf_lo(u[k]);
+                        v[1] -= bf_hi(u[k]);
+                    }
+                    stsm4(addr_a<TO>(so, 0, j * 8, lane), u);
                 }
+                __syncwarp();
+                constexpr int per = NH / 8;
+#pragma unroll
+                for (int k = 0; k < 16 * per / 32; ++k) {
+                    const int i = lane + k * 32, r = i / per, c = i % per;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(so + r * TO::pitch + c * 16)
+                                 : "memory");
+                    *reinterpret_cast<uint4*>(dst + p * kState + (pg * 16 + r) * N + n0 + c * 8) = v;
+                }
+            }
         }
         {
             const float tot = d.total;
@@ -208,10 +227,6 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
                     mma_planes<PC, PI>(S[j + 1], fa, fb[1]);
                 }
             }
-        }
-        if (warp == 0 && i + 1 < chunks) {
-            make_decays(i + 1);
-            if (i + 2 < chunks) fetch_dt(i + 2);
         }
     }
     float* dst = nullptr;
@@ -270,7 +285,7 @@ struct GradLayout {
     static constexpr int off_s0 = stages * stage_bytes, off_ds = off_s0 + (shared_state ? 0 : TS::bytes);
     static constexpr int off_b = off_ds + TS::bytes, off_c = off_b + TB::bytes;
     static constexpr int off_d = off_c + TB::bytes;
-    static constexpr int off_sc = off_d + 2 * static_cast<int>(sizeof(Decays));
+    static constexpr int off_sc = off_d + 3 * static_cast<int>(sizeof(Decays));  // the last head's until its end
     static constexpr int sc_floats = 7 * kChunk + 16;  // per head, twice
     static constexpr int bytes = off_sc + 2 * sc_floats * 4;
 };
@@ -377,20 +392,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
         const int h = h0 + i, s = stage(i);
         load_tile<TX, kScanP>(sb + s, xg + h * kScanP, a.ldx, nr, tid, kScanThreads);
         load_tile<TX, kScanP>(sb + s + TX::bytes, yg + h * kScanP, a.lddy, nr, tid, kScanThreads);
+        cp_decays(sb + LY::off_d + (i % 3) * static_cast<uint32_t>(sizeof(Decays)), a.dec + slot * a.H + h, tid);
     };
     auto load_states = [&](int i) {
         load_state(LY::off_s0, 0, h0 + i);
         if constexpr (!LY::shared_state) load_state(LY::off_ds, 1, h0 + i);
         cp_async_commit();
-    };
-    float dt0 = 0.f, dt1 = 0.f;  // warp 0: raw dt of the next head
-    auto fetch_dt = [&](int i) {
-        const long r = r0 + 2 * lane;
-        dt0 = r < r1 ? load_dt(a.dt, r * a.lddt + h0 + i, a.dt_bf16) : 0.f;
-        dt1 = r + 1 < r1 ? load_dt(a.dt, (r + 1) * a.lddt + h0 + i, a.dt_bf16) : 0.f;
-    };
-    auto make_decays = [&](int i) {
-        chunk_decays(dec[i & 1], dt0, dt1, nr, a.A[h0 + i], a.bias ? a.bias[h0 + i] : 0.f, a.softplus, lane);
     };
     auto sums = [&](int i) {
         float* p = reinterpret_cast<float*>(smem + LY::off_sc) + (i & 1) * LY::sc_floats;
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
     // Warp 0: from the row sums of head i to d dt and the chunk's part of dA, d dt_bias, dD.
     auto finish = [&](int i) {
         const HeadSums s = sums(i);
-        const Decays& d = dec[i & 1];
+        const Decays& d = dec[i % 3];
         const int h = h0 + i;
         float E[2], F[2];
 #pragma unroll
@@ -450,11 +457,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
                      tid, kScanThreads);
     load(0);
     load_states(0);
-    if (warp == 0) {
-        fetch_dt(0);
-        make_decays(0);
-        if (heads > 1) fetch_dt(1);
-    }
     cp_async_wait<0>();
     __syncthreads();
 
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             cp_async_wait<0>();
             __syncthreads();
         }
-        const Decays& d = dec[i & 1];
+        const Decays& d = dec[i % 3];
         const HeadSums hs = sums(i);
         const int ox = stage(i), oy = ox + TX::bytes;
         constexpr int os0 = LY::off_s0, ods = LY::off_ds;
@@ -732,14 +734,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
                 }
             }
         }
-        if (warp == 0) {
-            if (i > 0) finish(i - 1);
-            if (i + 1 < heads) {
-                __syncwarp();
-                make_decays(i + 1);
-                if (i + 2 < heads) fetch_dt(i + 2);
-            }
-        }
+        if (warp == 0 && i > 0) finish(i - 1);
     }
 
     // ---- + Q B (t side) or Q^T C (s side), and out
@@ -847,21 +842,22 @@ struct Plan {
     bool whole;
     long seg_count, chunk_count, rows;
     int shares;
-    size_t off_seg, off_decay, off_part, off_scalars, bytes;
+    size_t off_dec, off_seg, off_decay, off_part, off_scalars, bytes;
 };
 Plan plan_of(int B, int T, int H, int N, int G, int io_dtype, const int32_t* offs, bool packed) {
     Plan p;
     // both directions run at once; without segments the one pass makes states anyway
     p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, 296, 1.0, 1.0, 2.0});
     p.whole = p.seg.seg >= T;
-    p.chunk = SegMap{offs, B, T, kChunk, (T + kChunk - 1) / kChunk};
+    p.chunk = chunk_map(B, T, offs);
     p.seg_count = packed ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;
-    p.chunk_count = packed ? T / kChunk + B : static_cast<long>(B) * p.chunk.spb;
+    p.chunk_count = chunk_slots(B, T, packed);
     p.rows = packed ? T : static_cast<long>(B) * T;
     p.shares = shares_of(p.chunk_count, G, H / G);
         const size_t state = static_cast<size_t>(kScanP) * N;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-    p.off_seg = up(2 * static_cast<size_t>(p.chunk_count) * H * kStatePlanes * state * 2);
+    p.off_dec = up(2 * static_cast<size_t>(p.chunk_count) * H * kStatePlanes * state * 2);
+    p.off_seg = p.off_dec + up(static_cast<size_t>(p.chunk_count) * H * sizeof(Decays));
     p.off_decay = p.off_seg + (p.whole ? 0 : up(2 * static_cast<size_t>(p.seg_count) * H * state * 4));
     p.off_part = p.off_decay + (p.whole ? 0 : up(static_cast<size_t>(p.seg_count) * H * 4));
     p.off_scalars = p.off_part +
@@ -905,9 +901,9 @@ size_t scan_backward_workspace_bytes(int B, int T, int H, int N, int G, int io_d
 cudaError_t launch_scan_backward(const ScanBwdArgs& q, int io_dtype, cudaStream_t stream) {
     const Plan p = plan_of(q.B, q.T, q.H, q.N, q.G, io_dtype, q.seq_offsets, q.seq_offsets != nullptr);
     BwdDev d{};
-    d.x = q.x, d.dt = q.dt, d.Bm = q.Bm, d.Cm = q.Cm, d.dy = q.dy;
-    d.ldx = q.ldx, d.lddt = q.lddt, d.ldb = q.ldb, d.ldc = q.ldc, d.lddy = q.lddy;
-    d.A = q.A, d.D = q.D, d.bias = q.dt_bias, d.s0 = q.s0, d.dsT = q.dsT;
+    d.x = q.x, d.Bm = q.Bm, d.Cm = q.Cm, d.dy = q.dy;
+    d.ldx = q.ldx, d.ldb = q.ldb, d.ldc = q.ldc, d.lddy = q.lddy;
+    d.A = q.A, d.D = q.D, d.s0 = q.s0, d.dsT = q.dsT;
     d.dx = q.dx, d.ddt = q.ddt, d.dB = q.dB, d.dC = q.dC;
     d.lddx = q.lddx, d.ldddt = q.ldddt, d.lddb = q.lddb, d.lddc = q.lddc;
     d.dA = q.dA, d.dD = q.dD, d.dbias = q.ddt_bias, d.ds0 = q.ds0;
@@ -915,11 +911,16 @@ cudaError_t launch_scan_backward(const ScanBwdArgs& q, int io_dtype, cudaStream_
     d.seg = p.seg, d.chunk = p.chunk, d.seg_count = p.seg_count, d.chunk_count = p.chunk_count;
     uint8_t* ws = static_cast<uint8_t*>(q.ws);
     d.states = reinterpret_cast<__nv_bfloat16*>(ws);
+    Decays* dec = reinterpret_cast<Decays*>(ws + p.off_dec);
+    d.dec = dec;
     d.seg_state = reinterpret_cast<float*>(ws + p.off_seg);
     d.seg_decay = reinterpret_cast<float*>(ws + p.off_decay);
     d.part = reinterpret_cast<float*>(ws + p.off_part);
     d.scalars = reinterpret_cast<float*>(ws + p.off_scalars);
     d.shares = p.shares, d.rows = p.rows, d.status = q.status;
+    const cudaError_t e = launch_decays(
+        DecayArgs{q.dt, q.lddt, q.A, q.dt_bias, dec, q.H, q.softplus, d.dt_bf16, p.chunk, q.status}, stream);
+    if (e != cudaSuccess) return e;
     if (io_dtype == WKV7_BF16) switch (q.N) {
             case 16: return bwd_typed<__nv_bfloat16, 16>(d, p, stream);
             case 32: return bwd_typed<__nv_bfloat16, 32>(d, p, stream);

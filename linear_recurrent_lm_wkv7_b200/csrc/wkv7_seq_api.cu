@@ -174,7 +174,7 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
 
 size_t wkv7_selective_scan_workspace_bytes(int B, int T, int H, int D, int N, int packed) {
     if (scan_check(B, T, H, D, N, 1, WKV7_F32, WKV7_F32) != WKV7_OK) return 0;
-    return wkv7::scan_workspace_bytes(B, T, H, N, packed != 0);
+    return T > 0 ? wkv7::scan_workspace_bytes(B, T, H, N, packed != 0) : 0;
 }
 
 int wkv7_selective_scan(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt, const float* A, const void* Bm,
@@ -208,7 +208,7 @@ int wkv7_selective_scan(const void* x, int64_t ld_x, const void* dt, int64_t ld_
     int* status = nullptr;
     if (wkv7::device_status_word(&status) != WKV7_OK) return WKV7_ERR_CUDA;
     const wkv7::ScanArgs p{x,  ld_x, dt, ld_dt, A,  Bm, ld_b, Cm, ld_c, D_skip, dt_bias, s0, y, ld_y, sT,
-                           need ? static_cast<float*>(workspace) : nullptr, B, T, H, N, G, seq_offsets,
+                           workspace, B, T, H, N, G, seq_offsets,
                            dt_softplus ? 1 : 0, dt_dtype, status};
     return done(wkv7::launch_scan(p, io_dtype, cs));
 }

@@ -111,7 +111,9 @@ def test_scan_refusals(wk, step):
         need = wk.wkv7_selective_scan_workspace_bytes(1, 20000, 4, 64, 32, False)
         assert need > 0 and call(B=1, T=20000, ws=None) == -1 and call(B=1, T=20000, wsb=need - 1) == -1
         assert call(B=1, T=20000, wsb=need, ws=ok["y"]) == -1
-    assert wk.wkv7_selective_scan_workspace_bytes(1024, 64, 8, 64, 128, False) == 0
+    # the decays of every chunk and head (5 x 64 + 4 floats), even in one segment
+    assert wk.wkv7_selective_scan_workspace_bytes(1024, 64, 8, 64, 128, False) == 1024 * 8 * 324 * 4
+    assert wk.wkv7_selective_scan_workspace_bytes(4, 0, 8, 64, 128, True) == 0
     assert wk.wkv7_selective_scan_workspace_bytes(1, 64, 8, 32, 128, False) == 0
 
 
