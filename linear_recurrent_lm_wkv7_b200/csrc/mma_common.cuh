@@ -1,9 +1,9 @@
 // mma_common.cuh — warp-level bf16 products of the selective scan: fragments of
 // m16n8k16 with fp32 accumulation, fed by ldmatrix from padded shared-memory tiles.
 //
-// Values of more bits than bf16 are carried as a sum of bf16 planes, each the
-// rounding of what the planes before it left over: two planes hold 16 bits of
-// mantissa (relative error 2^-18), three hold 24.  A product of a P-plane by a
+// Values of more bits than bf16 are carried as a sum of bf16 planes, each holding the
+// leading bits of what the planes before it left over: two planes hold 16 bits of
+// mantissa (relative error 2^-16), three hold all 24.  A product of a P-plane by a
 // Q-plane value sums the plane products (i, j) with i + j < max(P, Q); what is left
 // out is below the last plane's rounding.
 //
@@ -55,17 +55,23 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two floats as bf16 planes: plane k holds the pair's k-th rounding, `lo` in the low half.
+// Two floats as bf16 planes, `lo` in the low half of a pair.  All planes but the last of
+// two are cut, not rounded (three planes hold 8 + 8 + 8 bits, a whole fp32): cutting is a
+// byte permutation, while the rounding conversion runs on the same quarter-rate unit as
+// the exponentials.
 template <int P>
 __device__ __forceinline__ void split_pair(uint32_t (&r)[P], float lo, float hi) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-        uint32_t u;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
-        r[k] = u;
-        if (k + 1 < P) {
-            lo -= __uint_as_float(u << 16);
-            hi -= __uint_as_float(u & 0xffff0000u);
+        if (P < 3 && k + 1 == P) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[k]) : "f"(hi), "f"(lo));
+        } else {
+            const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+            r[k] = __byte_perm(a, b, 0x7632);
+            if (k + 1 < P) {
+                lo -= __uint_as_float(a & 0xffff0000u);
+                hi -= __uint_as_float(b & 0xffff0000u);
+            }
         }
     }
 }

@@ -23,7 +23,7 @@ constexpr int kScanP = kHead;  // rows of the state
 constexpr int kScanThreads = 256;
 
 // Planes of an input; of fp32 values that only go into outputs of the io type (two
-// leave an error of 2^-18, far below the rounding to bf16); of those that go into
+// leave an error of 2^-16, far below the rounding to bf16); of those that go into
 // states and sums that stay fp32 (two left errors of 3e-6 in states, and of 2e-5 in dA
 // where its terms cancel).
 template <typename IO>
@@ -80,7 +80,33 @@ __device__ __forceinline__ bool seg_rows(const SegMap& m, long slot, int& n, lon
 }
 
 // ---------------------------------------------------------------- decays
-__device__ __forceinline__ float softplus_f32(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|), to a few 2^-24 of the value: the exponent of 2
+// as a sum of two floats, and log1p(t) = 2 artanh(t / (2 + t)) by its series (the argument
+// is at most 1/3, so the term z^17 / 17 left out is below 2^-30).  -inf gives 0, NaN NaN.
+__device__ __forceinline__ float softplus_f32(float x) {
+    const float m = -fabsf(x), h = m * 1.44269504f;
+    // -inf has no second part (its products would be NaN)
+    const float l = m > -1e30f ? fmaf(m, 1.92596299e-8f, fmaf(m, 1.44269504f, -h)) : 0.f;
+    const float t = ex2_ftz(h) * fmaf(l, 0.69314718f, 1.f);
+    const float den = 2.f + t, r = rcp_ftz(den);
+    const float q = t * r, z = fmaf(fmaf(-q, den, t), r, q), z2 = z * z;
+    float p = fmaf(z2, 1.f / 15.f, 1.f / 13.f);
+    p = fmaf(p, z2, 1.f / 11.f);
+    p = fmaf(p, z2, 1.f / 9.f);
+    p = fmaf(p, z2, 1.f / 7.f);
+    p = fmaf(p, z2, 1.f / 5.f);
+    p = fmaf(p, z2, 1.f / 3.f);
+    const float lg = 2.f * fmaf(z * z2, p, z);
+    return x > 0.f ? x + lg : x == x ? lg : x;
+}
+
+// 2^(h + l) for a small second part
+__device__ __forceinline__ float exp2_pair(float h, float l) { return ex2_ftz(h) * fmaf(l, 0.69314718f, 1.f); }
+// 2^(ah + al - bh - bl)
+__device__ __forceinline__ float exp2_diff(float ah, float al, float bh, float bl) {
+    const float s = ah - bh, v = s - ah;
+    return exp2_pair(s, (ah - (s - v)) - (bh + v) + (al - bl));  // s and its rounding error
+}
 
 // Per token of a chunk, in shared memory.  hi + lo = l_t log2(e).
 struct Decays {
@@ -94,12 +120,6 @@ struct Decays {
 // exp(l_t - l_s)
 __device__ __forceinline__ float decay_between(const Decays& d, int t, int s) {
     return ex2_ftz((d.hi[t] - d.hi[s]) + (d.lo[t] - d.lo[s]));
-}
-
-// 2^v for a 64-bit exponent: the part below the float's last place as a factor.
-__device__ __forceinline__ float exp2_f64(double v) {
-    const float h = static_cast<float>(v);
-    return ex2_ftz(h) * fmaf(static_cast<float>(v - h), 0.69314718f, 1.f);
 }
 
 // One warp: the decays of the chunk whose raw dt values lane l holds for tokens 2 l
@@ -127,14 +147,14 @@ __device__ __forceinline__ void chunk_decays(Decays& d, float dt0, float dt1, in
     if (lane == 0) before = 0.0;
     const double c0 = before + l0, c1 = before + l1;
     const double end = __shfl_sync(0xffffffffu, run, 31);
-    const float h0 = static_cast<float>(c0), h1 = static_cast<float>(c1);
+    const float h0 = static_cast<float>(c0), h1 = static_cast<float>(c1), he = static_cast<float>(end);
+    const float q0 = static_cast<float>(c0 - h0), q1 = static_cast<float>(c1 - h1), qe = static_cast<float>(end - he);
     *reinterpret_cast<float2*>(&d.delta[2 * lane]) = make_float2(e0, e1);
     *reinterpret_cast<float2*>(&d.hi[2 * lane]) = make_float2(h0, h1);
-    *reinterpret_cast<float2*>(&d.lo[2 * lane]) =
-        make_float2(static_cast<float>(c0 - h0), static_cast<float>(c1 - h1));
-    *reinterpret_cast<float2*>(&d.from[2 * lane]) = make_float2(exp2_f64(c0), exp2_f64(c1));
-    *reinterpret_cast<float2*>(&d.to[2 * lane]) = make_float2(exp2_f64(end - c0), exp2_f64(end - c1));
-    if (lane == 31) d.total = exp2_f64(end);
+    *reinterpret_cast<float2*>(&d.lo[2 * lane]) = make_float2(q0, q1);
+    *reinterpret_cast<float2*>(&d.from[2 * lane]) = make_float2(exp2_pair(h0, q0), exp2_pair(h1, q1));
+    *reinterpret_cast<float2*>(&d.to[2 * lane]) = make_float2(exp2_diff(he, qe, h0, q0), exp2_diff(he, qe, h1, q1));
+    if (lane == 31) d.total = exp2_pair(he, qe);
 }
 
 // The decays of every (chunk slot, head) of `map` (segments of one chunk): out [slot][H].

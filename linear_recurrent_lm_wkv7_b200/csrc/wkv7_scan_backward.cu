@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float* v = &rest[j + (k >> 1)][2 * (k & 1)];
-                        u[k] = pack_bf16(v[0], v[1]);
+                        u[k] = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x7632);
                         v[0] -= bf_lo(u[k]);
                         v[1] -= bf_hi(u[k]);
                     }

@@ -5,13 +5,13 @@
 // A block carries the state of one head through the chunks of one segment.  Per chunk:
 //   (1) G  = C B^T                      128 t x 128 s, K = 128
 //       M_ts = G_ts exp(l_t - l_s) delta_s, rounded to two bf16 planes in tensor memory
-//   (2) D1 = C S^T                      128 t x 64 p, K = 128, S as two bf16 planes
+//   (2) D1 = C S^T                      128 t x 2 x 64 p, K = 128, S as two bf16 planes side by side
 //   (3) D2 = M X                        128 t x 64 p, K = 128, A operand M from tensor memory
 //       y_t = exp(l_t) D1_t + D2_t + D x_t
 //   (4) D3 = B^T (X delta exp(l_128 - l))   128 n x 64 p, K = 128, the scaled x as three planes
 //       S <- exp(l_128) S + D3, in fp32 registers (lane n, 64 rows p)
 // Only (2) waits for the state, and the state only for (4): G, M and (4) of the next
-// chunk run ahead of it.  The outputs round to bf16, so two planes (2^-18) do for M and
+// chunk run ahead of it.  The outputs round to bf16, so two planes (2^-16) do for M and
 // the S of (2); the state stays fp32 and takes three.  D3 starts from zero at every chunk
 // and is added in fp32: the tensor cores cut their sums, and a state that was their
 // accumulator would lose 2^-23 at every step of a long sequence.
@@ -23,7 +23,6 @@
 //   20    loads (TMA);   21 issues every product;   22, 23 the decays of every other chunk
 //         (a chunk's take them some 5000 cycles of dependent steps, hence two, and three
 //         chunks' room)
-// The tensor work is 2304 cycles a chunk: 512 + 512 + 512 + 768.
 #include <cuda.h>
 
 #include "scan_common.cuh"
@@ -38,7 +37,10 @@ constexpr int kWarpS = 8, kWarpX = 16, kWarpLoad = 20, kWarpMma = 21, kWarpDec =
 constexpr int kTcThreads = 24 * 32;
 constexpr int kDecs = 3;  // chunks whose decays are kept
 constexpr int kHalf = kScanP / 2;
-constexpr uint64_t kWaitNs = 2000000000ull;
+// A wait gives up after kPolls polls of kPollNs: two seconds and more.  (A loop of its own,
+// and not the timed wait of sm100_ptx.cuh: there are dozens of waits, and with the clock's
+// reading in each the kernel's loops outgrew the instruction cache.)
+constexpr uint32_t kPollNs = 1000, kPolls = 1u << 21;
 
 constexpr uint32_t kTile = kL * 128;         // 128 rows of 128 bytes (64 bf16): one atom column
 constexpr uint32_t kStage = kTile + 4 * kTile;  // X, B (two atoms), C (two atoms)
@@ -55,18 +57,19 @@ struct Decays128 {
 };
 constexpr uint32_t kOffBar = kOffDec + kDecs * sizeof(Decays128);
 struct Bars {
-    uint64_t full[2], empty[2], dec_full[kDecs], dec_empty[kDecs], xw_full[2], xw_empty[2], d3_full[2];
-    uint64_t g_full, m_full, s_full, d1_full, d2_full, d_empty, fin;
+    uint64_t full[2], empty[2], dec_full[kDecs], dec_empty[kDecs], xw_full[2], xw_empty[2];
+    uint64_t d3_full, d3_empty, g_full, m_full, s_full, d1_full, d2_full, d_empty, fin;
     uint32_t tmem;
 };
 constexpr uint32_t kTcSmem = kOffBar + sizeof(Bars) + 1024;  // + alignment of the tiles
 static_assert(kTcSmem <= 227 * 1024, "shared memory of an SM");
 
 // tensor memory columns
-constexpr uint32_t kColG = 0, kColM = 128, kColD1 = 256, kColD2 = 320, kColD3 = 384;  // D3 twice
+constexpr uint32_t kColG = 0, kColM = 128, kColD1 = 256, kColD2 = 384, kColD3 = 448;  // D1: one half per plane of S
 
 constexpr uint32_t kIdG = idesc_f32acc(1, 128, 128, 0, 0);
-constexpr uint32_t kIdY = idesc_f32acc(1, 128, 64, 0, 1);   // A K-major (or tensor memory), B rows are K
+constexpr uint32_t kId1 = idesc_f32acc(1, 128, 128, 0, 1);  // A K-major, B rows are K: both planes of S
+constexpr uint32_t kIdY = idesc_f32acc(1, 128, 64, 0, 1);   // A from tensor memory, B rows are K
 constexpr uint32_t kIdS = idesc_f32acc(1, 128, 64, 1, 1);   // both rows are K
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t* bar, int c0, int c1) {
@@ -79,25 +82,49 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// A from tensor memory
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    const uint32_t z = 0;
+// One lane of the warp, always the same.  The products' warp runs converged and only the
+// instructions themselves are that lane's: their descriptors then stay in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+// d (+)= a b: A from shared memory, or from tensor memory
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(z), "r"(z), "r"(z), "r"(z));
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)));
 }
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)));
+}
+// 16 columns of this lane; several loads, then one wait that their results go through.
 __device__ __forceinline__ void tmem_load16(uint32_t taddr, float (&f)[16]) {
-    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]),
           "=f"(f[8]), "=f"(f[9]), "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
         : "r"(taddr)
         : "memory");
+}
+// Waits for the loads; the values may only be used behind it.
+__device__ __forceinline__ void tmem_wait(float (&f)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
+                   "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]),
+                   "+f"(f[15])::"memory");
 }
 __device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&f)[8]) {
     __syncwarp();
@@ -114,7 +141,8 @@ __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::
 // no time to build descriptors.
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return sdesc_sw128(addr, 16, 1024); }
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) { return sdesc_sw128(addr, lbo, 1024); }
-__host__ __device__ constexpr uint64_t step_k(int k) { return (k >> 2) * (kTile >> 4) + (k & 3) * 2; }
+// from K-step k to the next: 32 bytes on, or from the first atom column's last to the second's first
+__host__ __device__ constexpr uint64_t next_k(int k) { return k == 3 ? (kTile >> 4) - 6 : 2; }
 __host__ __device__ constexpr uint64_t step_mn(int k) { return k * 128; }
 __host__ __device__ constexpr uint64_t at(uint32_t bytes) { return bytes >> 4; }  // further on in shared memory
 
@@ -155,21 +183,22 @@ __device__ __forceinline__ void chunk_decays128(Decays128& d, const float (&dt)[
     double before = __shfl_up_sync(0xffffffffu, run, 1);
     if (lane == 0) before = 0.0;
     const double end = __shfl_sync(0xffffffffu, run, 31);
+    const float he = static_cast<float>(end), le = static_cast<float>(end - he);
     float hi[4], lo[4], from[4], w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const double c = before + l[i];
         hi[i] = static_cast<float>(c);
         lo[i] = static_cast<float>(c - hi[i]);
-        from[i] = exp2_f64(c);
-        w[i] = e[i] * exp2_f64(end - c);
+        from[i] = exp2_pair(hi[i], lo[i]);
+        w[i] = e[i] * exp2_diff(he, le, hi[i], lo[i]);
     }
     *reinterpret_cast<float4*>(&d.delta[4 * lane]) = make_float4(e[0], e[1], e[2], e[3]);
     *reinterpret_cast<float4*>(&d.hi[4 * lane]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<float4*>(&d.lo[4 * lane]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
     *reinterpret_cast<float4*>(&d.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
     *reinterpret_cast<float4*>(&d.w[4 * lane]) = make_float4(w[0], w[1], w[2], w[3]);
-    if (lane == 31) d.total = exp2_f64(end);
+    if (lane == 31) d.total = exp2_pair(he, le);
 }
 
 // OUT, whole: as in scan_kernel (wkv7_scan.cu).
@@ -181,7 +210,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t sb = smem_u32(sm);
     Bars& bar = *reinterpret_cast<Bars*>(sm + kOffBar);
     Decays128* dec = reinterpret_cast<Decays128*>(sm + kOffDec);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same for all lanes, and known to be
     const int h = blockIdx.x % a.H, grp = h / (a.H / a.G);
     const long slot = blockIdx.x / a.H;
     constexpr long kState = static_cast<long>(kScanP) * kN;
@@ -207,12 +237,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_init(&bar.empty[i], OUT ? 9 : 1);
                 mbar_init(&bar.xw_full[i], 4);
                 mbar_init(&bar.xw_empty[i], 1);
-                mbar_init(&bar.d3_full[i], 1);
             }
             for (int i = 0; i < kDecs; ++i) {
                 mbar_init(&bar.dec_full[i], 1);
                 mbar_init(&bar.dec_empty[i], OUT ? 20 : 12);
             }
+            mbar_init(&bar.d3_full, 1);
+            mbar_init(&bar.d3_empty, 8);
             mbar_init(&bar.g_full, 1);
             mbar_init(&bar.m_full, 8);
             mbar_init(&bar.s_full, 8);
@@ -231,11 +262,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tm = bar.tmem;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lanes 32 (warp % 4) ..
     bool ok = true;
-    // Waits for phase number `k` (0, 1, ..) of a barrier, for a limited time: one lane polls,
-    // and the warp goes on or gives up as one.
+    // Waits for phase number `k` (0, 1, ..) of a barrier: the warp goes on or gives up as one.
     auto wait = [&](uint64_t& b, int k) {
-        const bool done = !ok || lane != 0 || mbar_wait(&b, static_cast<uint32_t>(k) & 1u, kWaitNs);
-        ok = __all_sync(0xffffffffu, done) && ok;
+        for (uint32_t i = 0; ok && !__all_sync(0xffffffffu, mbar_try_wait_sleep(&b, k & 1, kPollNs)); ++i)
+            ok = i < kPolls;
     };
     auto signal = [&](uint64_t& b) {  // once per warp
         __syncwarp();
@@ -266,36 +296,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
                 const Decays128& d = dec[c % kDecs];
                 const float ht = d.hi[t], lt = d.lo[t];
-                for (int j = half; j <= q; j += 2)
+                // pieces of 16 columns: two to a block of 32, blocks half, half + 2 up to q
+                const int pieces = q >= half ? 2 * ((q - half) / 2 + 1) : 0;
+                auto col = [&](int i) { return 32 * (half + 2 * (i >> 1)) + 16 * (i & 1); };
+                float g[16], nx[16];
+                __syncwarp();
+                if (pieces) tmem_load16(tG + col(0), nx);
+#pragma unroll 1
+                for (int i = 0; i < pieces; ++i) {
+                    const int s0 = col(i);
+                    tmem_wait(nx);
 #pragma unroll
-                    for (int b = 0; b < 32; b += 16) {
-                        float g[16];
-                        tmem_load16(tG + 32 * j + b, g);
-                        uint32_t p0[8], p1[8];
+                    for (int e = 0; e < 16; ++e) g[e] = nx[e];
+                    if (i + 1 < pieces) tmem_load16(tG + col(i + 1), nx);
+                    uint32_t p0[8], p1[8];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const int s = 32 * j + b + i;
-                            const float4 hs = *reinterpret_cast<const float4*>(&d.hi[s]);
-                            const float4 ls = *reinterpret_cast<const float4*>(&d.lo[s]);
-                            const float4 ds = *reinterpret_cast<const float4*>(&d.delta[s]);
-                            float m[4];
-                            m[0] = g[i] * (ex2_ftz((ht - hs.x) + (lt - ls.x)) * ds.x);
-                            m[1] = g[i + 1] * (ex2_ftz((ht - hs.y) + (lt - ls.y)) * ds.y);
-                            m[2] = g[i + 2] * (ex2_ftz((ht - hs.z) + (lt - ls.z)) * ds.z);
-                            m[3] = g[i + 3] * (ex2_ftz((ht - hs.w) + (lt - ls.w)) * ds.w);
-                            if (j == q) {
+                    for (int k = 0; k < 16; k += 4) {
+                        const int s = s0 + k;
+                        const float4 hs = *reinterpret_cast<const float4*>(&d.hi[s]);
+                        const float4 ls = *reinterpret_cast<const float4*>(&d.lo[s]);
+                        const float4 ds = *reinterpret_cast<const float4*>(&d.delta[s]);
+                        float m[4];
+                        m[0] = g[k] * (ex2_ftz((ht - hs.x) + (lt - ls.x)) * ds.x);
+                        m[1] = g[k + 1] * (ex2_ftz((ht - hs.y) + (lt - ls.y)) * ds.y);
+                        m[2] = g[k + 2] * (ex2_ftz((ht - hs.z) + (lt - ls.z)) * ds.z);
+                        m[3] = g[k + 3] * (ex2_ftz((ht - hs.w) + (lt - ls.w)) * ds.w);
+                        if (s0 + 16 > 32 * q) {
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) m[e] = s + e <= t ? m[e] : 0.f;
-                            }
-                            uint32_t u[2];
-                            split_pair<2>(u, m[0], m[1]);
-                            p0[i / 2] = u[0], p1[i / 2] = u[1];
-                            split_pair<2>(u, m[2], m[3]);
-                            p0[i / 2 + 1] = u[0], p1[i / 2 + 1] = u[1];
+                            for (int e = 0; e < 4; ++e) m[e] = s + e <= t ? m[e] : 0.f;
                         }
-                        tmem_store8(tM + 16 * j + b / 2, p0);
-                        tmem_store8(tM + 64 + 16 * j + b / 2, p1);
+                        uint32_t u[2];
+                        split_pair<2>(u, m[0], m[1]);
+                        p0[k / 2] = u[0], p1[k / 2] = u[1];
+                        split_pair<2>(u, m[2], m[3]);
+                        p0[k / 2 + 1] = u[0], p1[k / 2 + 1] = u[1];
                     }
+                    tmem_store8(tM + s0 / 2, p0);
+                    tmem_store8(tM + 64 + s0 / 2, p1);
+                }
                 tmem_store_wait();
                 tc_fence_before();
                 signal(bar.m_full);
@@ -332,20 +370,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int c = 0; c < chunks && ok; ++c) {
             const Decays128& d = dec[c % kDecs];
             wait(bar.dec_full[c % kDecs], c / kDecs);
-            wait(bar.d3_full[c & 1], c >> 1);
+            wait(bar.d3_full, c);
             if (!ok) break;
             tc_fence_after();
             const float tot = d.total, f = d.from[row];
             signal(bar.dec_empty[c % kDecs]);
             run *= tot;
+            {
+                float v[2][16];
+                __syncwarp();
+                tmem_load16(tm + lane_base + kColD3 + p0, v[0]);
+                tmem_load16(tm + lane_base + kColD3 + p0 + 16, v[1]);
+                tmem_wait(v[0]);
+                tmem_wait(v[1]);
 #pragma unroll
-            for (int i = 0; i < kHalf; i += 16) {
-                float v[16];
-                tmem_load16(tm + lane_base + kColD3 + 64 * (c & 1) + p0 + i, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) S[i + e] = fmaf(tot, S[i + e], v[e]);
+                for (int e = 0; e < kHalf; ++e) S[e] = fmaf(tot, S[e], v[e / 16][e % 16]);
             }
             tc_fence_before();
+            signal(bar.d3_empty);
             if constexpr (OUT) {
                 wait(bar.d1_full, c);  // (2) has read the planes
                 if (!ok) break;
@@ -356,11 +398,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint8_t* xs = sm + (c & 1) * kStage;
                 __nv_bfloat16* dst = a.y + (r0 + static_cast<long>(c) * kL + row) * a.ldy + h * kScanP + p0;
                 const bool live = row < count(c);
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < kHalf; i += 16) {
                     float u[16], v[16];
-                    tmem_load16(tm + lane_base + kColD1 + p0 + i, u);
-                    tmem_load16(tm + lane_base + kColD2 + p0 + i, v);
+                    {
+                        float w[16];
+                        __syncwarp();
+                        tmem_load16(tm + lane_base + kColD1 + p0 + i, u);
+                        tmem_load16(tm + lane_base + kColD1 + 64 + p0 + i, w);
+                        tmem_load16(tm + lane_base + kColD2 + p0 + i, v);
+                        tmem_wait(u);
+                        tmem_wait(w);
+                        tmem_wait(v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) u[e] += w[e];
+                    }
                     if (i == kHalf - 16) {
                         tc_fence_before();
                         signal(bar.d_empty);
@@ -395,6 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* st = sm + (c & 1) * kStage;
             wait(bar.full[c & 1], c >> 1);
             wait(bar.dec_full[c % kDecs], c / kDecs);
+#pragma unroll 1
             for (int k = 0; k < 4 && ok; ++k) {
                 const int piece = 4 * c + k, s = 32 * k + r;
                 if (piece >= 2) wait(bar.xw_empty[piece & 1], (piece >> 1) - 1);
@@ -453,7 +506,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // nothing may still be on its way into shared memory when the block ends
         if (!ok)
             for (int c = issued < 2 ? 0 : issued - 2; c < issued; ++c)
-                mbar_wait(&bar.full[c & 1], static_cast<uint32_t>(c >> 1) & 1u, kWaitNs);
+                mbar_wait(&bar.full[c & 1], static_cast<uint32_t>(c >> 1) & 1u, 2000000000ull);
     } else if (warp >= kWarpDec) {
         // ------------------------------------------------------------ decays
         const float Ah = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
@@ -473,75 +526,101 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fetch(c + 2);
             signal(bar.dec_full[c % kDecs]);
         }
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------------ products
-        auto wait1 = [&](uint64_t& b, int k) { ok = ok && mbar_wait(&b, static_cast<uint32_t>(k) & 1u, kWaitNs); };
         const uint64_t dX = desc_mn(sb, kTile), dBk = desc_k(sb + kTile), dBn = desc_mn(sb + kTile, kTile),
                        dC = desc_k(sb + 3 * kTile), dS = desc_mn(sb + kOffS, kTile), dXw = desc_mn(sb + kOffXw, kPiece);
         auto products_g = [&](int c) {
             const uint64_t st = (c & 1) * at(kStage);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                mma_ss<false>(tm + kColG, dC + st + step_k(k), dBk + st + step_k(k), kIdG, k > 0);
-            mma_commit(&bar.g_full);
+            if (elect_one()) {
+                uint64_t p = dC + st, q = dBk + st;
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    mma_smem(tm + kColG, p, q, kIdG, k > 0);
+                    const uint64_t d = next_k(k);
+                    p += d;
+                    q += d;
+                }
+                mma_commit(&bar.g_full);
+            }
+            __syncwarp();
         };
         for (int c = 0; c < chunks && ok; ++c) {
             const int st = c & 1;
             const uint64_t so = st * at(kStage);
             if (!OUT || c == 0) {
-                wait1(bar.full[st], c >> 1);
+                wait(bar.full[st], c >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (OUT) products_g(0);
             }
-            // (4)
-            const uint32_t d3 = tm + kColD3 + 64 * st;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int piece = 4 * c + k;
-                wait1(bar.xw_full[k & 1], piece >> 1);
-                if (!ok) break;
+            // (4), half of its pieces at a time: the ring is filled again while (2) runs
+            if (c > 0) wait(bar.d3_empty, c - 1);
+            auto products_s = [&](int k) {
+                wait(bar.xw_full[k & 1], (4 * c + k) >> 1);
+                if (!ok) return;
                 tc_fence_after();
-#pragma unroll
-                for (int p = 0; p < 3; ++p)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        mma_ss<false>(d3, dBn + so + step_mn(2 * k + j),
-                                      dXw + at((k & 1) * 3 * kPiece + p * kPiece) + step_mn(j), kIdS,
-                                      k > 0 || p > 0 || j > 0);
-                mma_commit(&bar.xw_empty[k & 1]);
-            }
-            if (!ok) break;
-            mma_commit(&bar.d3_full[st]);
-            if constexpr (!OUT) {
-                mma_commit(&bar.empty[st]);
-            } else {
+                if (elect_one()) {
+                    const uint64_t p = dBn + so + step_mn(2 * k);
+                    uint64_t q = dXw + (k & 1) * at(3 * kPiece);
+#pragma unroll 1
+                    for (int i = 0; i < 3; ++i, q += at(kPiece)) {
+                        mma_smem(tm + kColD3, p, q, kIdS, k > 0 || i > 0);
+                        mma_smem(tm + kColD3, p + step_mn(1), q + step_mn(1), kIdS, true);
+                    }
+                    mma_commit(&bar.xw_empty[k & 1]);
+                    if (k == 3) {
+                        mma_commit(&bar.d3_full);
+                        if constexpr (!OUT) mma_commit(&bar.empty[st]);
+                    }
+                }
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) products_s(k);
+            if constexpr (OUT) {
                 // (2)
-                wait1(bar.s_full, c);
-                if (c > 0) wait1(bar.d_empty, c - 1);
+                wait(bar.s_full, c);
+                if (c > 0) wait(bar.d_empty, c - 1);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ss<false>(tm + kColD1, dC + so + step_k(k), dS + at(p * kTile) + step_mn(k), kIdY,
-                                      p > 0 || k > 0);
-                mma_commit(&bar.d1_full);
+                if (elect_one()) {
+                    uint64_t p = dC + so, q = dS;
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        mma_smem(tm + kColD1, p, q, kId1, k > 0);
+                        p += next_k(k);
+                        q += step_mn(1);
+                    }
+                    mma_commit(&bar.d1_full);
+                }
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int k = 2; k < 4; ++k) products_s(k);
+            if (!ok) break;
+            if constexpr (OUT) {
                 // (3)
-                wait1(bar.m_full, c);
+                wait(bar.m_full, c);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(tm + kColD2, tm + kColM + 64 * p + 8 * k, dX + so + step_mn(k), kIdY, p > 0 || k > 0);
-                mma_commit(&bar.d2_full);
-                mma_commit(&bar.empty[st]);
+                if (elect_one()) {
+                    uint32_t p = tm + kColM;
+                    uint64_t q = dX + so;
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        mma_tmem(tm + kColD2, p, q, kIdY, k > 0);
+                        mma_tmem(tm + kColD2, p + 64, q, kIdY, true);
+                        p += 8;
+                        q += step_mn(1);
+                    }
+                    mma_commit(&bar.d2_full);
+                    mma_commit(&bar.empty[st]);
+                }
+                __syncwarp();
                 // (1) of the next chunk: M of this one has been made, so G is free
                 if (c + 1 < chunks) {
-                    wait1(bar.full[st ^ 1], (c + 1) >> 1);
+                    wait(bar.full[st ^ 1], (c + 1) >> 1);
                     if (!ok) break;
                     tc_fence_after();
                     products_g(c + 1);
@@ -549,8 +628,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         // every product is complete before tensor memory is given back
-        mma_commit(&bar.fin);
-        ok = mbar_wait(&bar.fin, 0, kWaitNs) && ok;
+        if (elect_one()) mma_commit(&bar.fin);
+        __syncwarp();
+        const bool before = ok;
+        ok = true;
+        wait(bar.fin, 0);
+        ok = ok && before;
     }
     __syncwarp();
     if (!ok && lane == 0) report_status(a.status, WKV7_ERR_DEVICE_TIMEOUT);
