@@ -55,22 +55,57 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 // Two floats as bf16 planes, `lo` in the low half of a pair.  All planes but the last of
 // two are cut, not rounded (three planes hold 8 + 8 + 8 bits, a whole fp32): cutting is a
 // byte permutation, while the rounding conversion runs on the same quarter-rate unit as
 // the exponentials.
-template <int P>
+// CUT = false rounds every plane: for products of two values in planes each, where the
+// products left out would add up with one sign.
+template <int P, bool CUT = true>
 __device__ __forceinline__ void split_pair(uint32_t (&r)[P], float lo, float hi) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-        if (P < 3 && k + 1 == P) {
+        if (!CUT) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[k]) : "f"(hi), "f"(lo));
+            if (k + 1 < P) {
+                lo -= __uint_as_float(r[k] << 16);
+                hi -= __uint_as_float(r[k] & 0xffff0000u);
+            }
+        } else if (P < 3 && k + 1 == P) {
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[k]) : "f"(hi), "f"(lo));
         } else {
             const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
             r[k] = __byte_perm(a, b, 0x7632);
-            if (k + 1 < P) {
-                lo -= __uint_as_float(a & 0xffff0000u);
-                hi -= __uint_as_float(b & 0xffff0000u);
+            if (k + 1 < P) {  // x + (-cut(x)): the sign bit is cut(x)'s top bit
+                const float2 v = add2(make_float2(lo, hi), make_float2(__uint_as_float((a & 0xffff0000u) ^ 0x80000000u),
+                                                                       __uint_as_float((b & 0xffff0000u) ^ 0x80000000u)));
+                lo = v.x, hi = v.y;
             }
         }
     }

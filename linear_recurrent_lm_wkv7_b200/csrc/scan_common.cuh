@@ -9,7 +9,7 @@
 //   y_t = sum_{s<=t} exp(l_t - l_s) (C_t . B_s) delta_s x_s + exp(l_t) S_0 C_t + D x_t
 //   S_64 = exp(l_64) S_0 + sum_s exp(l_64 - l_s) delta_s x_s B_s^T
 // Only differences l_t - l_s with s <= t are exponentiated, so nothing overflows that
-// the recurrence itself would not.  l is summed in 64 bits and kept as two floats:
+// the recurrence itself would not.  l is summed and kept as two floats:
 // behind strong decays (|l| of thousands) the difference of two neighbours still
 // has 32 bits.
 #pragma once
@@ -100,6 +100,35 @@ __device__ __forceinline__ float softplus_f32(float x) {
     return x > 0.f ? x + lg : x == x ? lg : x;
 }
 
+// A sum of two floats, the second below the first's last place.
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+    const float s = a.h + b.h, v = s - a.h;
+    const float l = (a.h - (s - v)) + (b.h - v) + (a.l + b.l);  // what s lost, and the second parts
+    const float r = s + l;
+    return {r, l - (r - s)};
+}
+__device__ __forceinline__ Pair pair_mul(float x, Pair a) {
+    const float p = x * a.h;
+    return {p, fmaf(x, a.l, fmaf(x, a.h, -p))};
+}
+// A log2(e)
+__device__ __forceinline__ Pair log2_rate(float A) {
+    return {A * 1.44269504f, fmaf(A, 1.92596299e-8f, fmaf(A, 1.44269504f, -(A * 1.44269504f)))};
+}
+// Sums over this lane's value and those of the lanes before it.
+__device__ __forceinline__ Pair pair_scan(Pair v, int lane) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const Pair o{__shfl_up_sync(0xffffffffu, v.h, m), __shfl_up_sync(0xffffffffu, v.l, m)};
+        const Pair t = pair_add(o, v);
+        if (lane >= m) v = t;
+    }
+    return v;
+}
+
 // 2^(h + l) for a small second part
 __device__ __forceinline__ float exp2_pair(float h, float l) { return ex2_ftz(h) * fmaf(l, 0.69314718f, 1.f); }
 // 2^(ah + al - bh - bl)
@@ -133,28 +162,19 @@ __device__ __forceinline__ void chunk_decays(Decays& d, float dt0, float dt1, in
     }
     if (2 * lane >= n) e0 = 0.f;
     if (2 * lane + 1 >= n) e1 = 0.f;
-    constexpr double kLog2e = 1.4426950408889634074;
-    const double s = static_cast<double>(A) * kLog2e;
-    const double l0 = e0 * s;
-    double l1 = l0 + e1 * s;
-    double run = l1;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, run, m);
-        if (lane >= m) run += o;
-    }
-    double before = __shfl_up_sync(0xffffffffu, run, 1);
-    if (lane == 0) before = 0.0;
-    const double c0 = before + l0, c1 = before + l1;
-    const double end = __shfl_sync(0xffffffffu, run, 31);
-    const float h0 = static_cast<float>(c0), h1 = static_cast<float>(c1), he = static_cast<float>(end);
-    const float q0 = static_cast<float>(c0 - h0), q1 = static_cast<float>(c1 - h1), qe = static_cast<float>(end - he);
+    const Pair rate = log2_rate(A), l0 = pair_mul(e0, rate), l1 = pair_add(l0, pair_mul(e1, rate));
+    const Pair run = pair_scan(l1, lane);
+    Pair before{__shfl_up_sync(0xffffffffu, run.h, 1), __shfl_up_sync(0xffffffffu, run.l, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Pair end{__shfl_sync(0xffffffffu, run.h, 31), __shfl_sync(0xffffffffu, run.l, 31)};
+    const Pair c0 = pair_add(before, l0), c1 = run;
     *reinterpret_cast<float2*>(&d.delta[2 * lane]) = make_float2(e0, e1);
-    *reinterpret_cast<float2*>(&d.hi[2 * lane]) = make_float2(h0, h1);
-    *reinterpret_cast<float2*>(&d.lo[2 * lane]) = make_float2(q0, q1);
-    *reinterpret_cast<float2*>(&d.from[2 * lane]) = make_float2(exp2_pair(h0, q0), exp2_pair(h1, q1));
-    *reinterpret_cast<float2*>(&d.to[2 * lane]) = make_float2(exp2_diff(he, qe, h0, q0), exp2_diff(he, qe, h1, q1));
-    if (lane == 31) d.total = exp2_pair(he, qe);
+    *reinterpret_cast<float2*>(&d.hi[2 * lane]) = make_float2(c0.h, c1.h);
+    *reinterpret_cast<float2*>(&d.lo[2 * lane]) = make_float2(c0.l, c1.l);
+    *reinterpret_cast<float2*>(&d.from[2 * lane]) = make_float2(exp2_pair(c0.h, c0.l), exp2_pair(c1.h, c1.l));
+    *reinterpret_cast<float2*>(&d.to[2 * lane]) =
+        make_float2(exp2_diff(end.h, end.l, c0.h, c0.l), exp2_diff(end.h, end.l, c1.h, c1.l));
+    if (lane == 31) d.total = exp2_pair(end.h, end.l);
 }
 
 // The decays of every (chunk slot, head) of `map` (segments of one chunk): out [slot][H].
@@ -218,8 +238,8 @@ struct TileRegs {
         for (int k = 0; k < count; ++k) {
             const int i = tid + k * THREADS, r = i / per, c = i % per;
             uint32_t a[TL::planes], b[TL::planes];
-            split_pair<TL::planes>(a, v[k].x, v[k].y);
-            split_pair<TL::planes>(b, v[k].z, v[k].w);
+            split_pair<TL::planes, false>(a, v[k].x, v[k].y);
+            split_pair<TL::planes, false>(b, v[k].z, v[k].w);
 #pragma unroll
             for (int p = 0; p < TL::planes; ++p) sts64(dst + p * TL::plane + r * TL::pitch + c * 8, a[p], b[p]);
         }
@@ -250,7 +270,7 @@ __device__ __forceinline__ void scale_frag(uint32_t (&out)[POUT][4], const uint3
             hi += bf_hi(in[p][r]);
         }
         uint32_t u[POUT];
-        split_pair<POUT>(u, lo * (r < 2 ? f0 : f8), hi * (r < 2 ? f1 : f9));
+        split_pair<POUT, PIN == 1>(u, lo * (r < 2 ? f0 : f8), hi * (r < 2 ? f1 : f9));
 #pragma unroll
         for (int p = 0; p < POUT; ++p) out[p][r] = u[p];
     }

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
                         const float m1 =
                             t >= s + 1 ? acc[j][2 * r + 1] * decay_between(d, t, s + 1) * d.delta[s + 1] : 0.f;
                         uint32_t pl[PC];
-                        split_pair<PC>(pl, m0, m1);
+                        split_pair<PC, PI == 1>(pl, m0, m1);
 #pragma unroll
                         for (int p = 0; p < PC; ++p) sts32(sM + p * TM::plane + t * TM::pitch + s * 2, pl[p]);
                     }
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float* s = &S[2 * kk + (r >> 1)][2 * (r & 1)];
-                        split_pair<PC>(u, s[0], s[1]);
+                        split_pair<PC, PI == 1>(u, s[0], s[1]);
 #pragma unroll
                         for (int p = 0; p < PC; ++p) fa[p][r] = u[p];
                     }
@@ -413,13 +413,23 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanDev a, int ele
     const long first = seg_first(a.map, static_cast<int>(n), lo), cnt = (hi - lo + a.map.seg - 1) / a.map.seg;
     const long st = (n * a.H + h) * elems + e;
     float4 S = a.s0 ? *reinterpret_cast<const float4*>(a.s0 + st) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long i = 0; i < cnt; ++i) {
-        const long u = (first + i) * a.H + h;
-        float4* p = reinterpret_cast<float4*>(a.seg_state + u * elems + e);
-        const float4 v = *p;
-        const float f = a.seg_decay[u];
-        *p = S;
-        S.x = fmaf(f, S.x, v.x), S.y = fmaf(f, S.y, v.y), S.z = fmaf(f, S.z, v.z), S.w = fmaf(f, S.w, v.w);
+    auto at = [&](long i) { return reinterpret_cast<float4*>(a.seg_state + ((first + i) * a.H + h) * elems + e); };
+    for (long i = 0; i < cnt; i += 4) {  // four segments' loads before the first is used
+        float4 v[4];
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < cnt) {
+                v[k] = *at(i + k);
+                f[k] = a.seg_decay[(first + i + k) * a.H + h];
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < cnt) {
+                *at(i + k) = S;
+                S.x = fmaf(f[k], S.x, v[k].x), S.y = fmaf(f[k], S.y, v[k].y);
+                S.z = fmaf(f[k], S.z, v[k].z), S.w = fmaf(f[k], S.w, v[k].w);
+            }
     }
     if (a.sT) *reinterpret_cast<float4*>(a.sT + st) = S;
 }

@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float* v = &rest[j + (k >> 1)][2 * (k & 1)];
-                        u[k] = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x7632);
+                        u[k] = PI == 1 ? __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x7632)
+                                       : pack_bf16(v[0], v[1]);
                         v[0] -= bf_lo(u[k]);
                         v[1] -= bf_hi(u[k]);
                     }
@@ -320,13 +321,13 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 // Two neighbouring accumulator tiles [16][16] as planes of an A fragment.
-template <int P>
+template <int P, bool CUT>
 __device__ __forceinline__ void acc_to_a(uint32_t (&f)[P][4], const float (&t0)[4], const float (&t1)[4]) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const float* s = (r < 2 ? t0 : t1) + 2 * (r & 1);
         uint32_t u[P];
-        split_pair<P>(u, s[0], s[1]);
+        split_pair<P, CUT>(u, s[0], s[1]);
 #pragma unroll
         for (int p = 0; p < P; ++p) f[p][r] = u[p];
     }
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             for (int c = 0; c < 4; ++c) {
                 if (c > blk) continue;
                 uint32_t fa[kStatePlanes][4];
-                acc_to_a<kStatePlanes>(fa, M[2 * c], M[2 * c + 1]);
+                acc_to_a<kStatePlanes, true>(fa, M[2 * c], M[2 * c + 1]);
 #pragma unroll
                 for (int j = 2 * c; j < 8; ++j) {
                     if (j > 2 * blk + 1) continue;
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             for (int c = 0; c < 4; ++c) {
                 if (!in_tri(c)) continue;
                 uint32_t fa[PC][4];
-                acc_to_a<PC>(fa, M[2 * c], M[2 * c + 1]);
+                acc_to_a<PC, PI == 1>(fa, M[2 * c], M[2 * c + 1]);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     uint32_t fb[2][PI][2];
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
     for (int c = 0; c < 4; ++c) {
         if (!in_tri(c)) continue;
         uint32_t fa[PC][4];
-        acc_to_a<PC>(fa, Q[2 * c], Q[2 * c + 1]);
+        acc_to_a<PC, PI == 1>(fa, Q[2 * c], Q[2 * c + 1]);
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
             uint32_t fb[2][PI][2];

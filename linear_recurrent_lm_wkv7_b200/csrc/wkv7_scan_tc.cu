@@ -19,10 +19,12 @@
 // 24 warps, each on one job, in step through mbarriers:
 //   0-7   M from G (row t per lane; the 32 x 32 blocks of the lower triangle, shared by two warps)
 //   8-15  the state (lane n, half of p each), its planes, and y (lane t)
-//   16-19 the scaled x, in pieces of 32 tokens through a ring of two
-//   20    loads (TMA);   21 issues every product;   22, 23 the decays of every other chunk
-//         (a chunk's take them some 5000 cycles of dependent steps, hence two, and three
-//         chunks' room)
+//   16-18, 20  the scaled x, in pieces of 32 tokens through a ring of two
+//   19    loads (TMA);   21 issues every product;   22, 23 the decays of every other chunk
+//         (thousands of cycles of dependent steps each, hence two, and three chunks' room)
+// Lanes 32 (w % 4) .. of tensor memory belong to warps w, and so does the SM's quarter that
+// they issue on: warps 3 and 7 make four blocks of M, warps 0 and 4 one.  The jobs that
+// touch no tensor memory are therefore put on the first quarters.
 #include <cuda.h>
 
 #include "scan_common.cuh"
@@ -33,7 +35,7 @@ namespace {
 
 constexpr int kL = 128;         // tokens per chunk
 constexpr int kN = 128;         // columns of the state
-constexpr int kWarpS = 8, kWarpX = 16, kWarpLoad = 20, kWarpMma = 21, kWarpDec = 22;
+constexpr int kWarpS = 8, kWarpX = 16, kWarpLoad = 19, kWarpMma = 21, kWarpDec = 22;
 constexpr int kTcThreads = 24 * 32;
 constexpr int kDecs = 3;  // chunks whose decays are kept
 constexpr int kHalf = kScanP / 2;
@@ -47,18 +49,21 @@ constexpr uint32_t kStage = kTile + 4 * kTile;  // X, B (two atoms), C (two atom
 constexpr uint32_t kOffS = 2 * kStage;       // two planes of S^T: rows n, 64 p
 constexpr uint32_t kPiece = 32 * 128;        // 32 tokens of scaled x, one plane
 constexpr uint32_t kOffXw = kOffS + 2 * kTile;
+// the pass that only makes states has no planes of S: its ring starts there and holds four
+constexpr uint32_t kOffXwStates = kOffS;
 constexpr uint32_t kOffDec = kOffXw + 2 * 3 * kPiece;
+static_assert(kOffXwStates + 4 * 3 * kPiece <= kOffDec, "the ring of four");
 
 struct Decays128 {
-    float delta[kL], hi[kL], lo[kL];  // hi + lo = l_t log2(e)
+    float delta[kL], hi[kL], lo[kL];  // hi + lo = -l_t log2(e): negated, to be added
     float from[kL];                   // exp(l_t)
     float w[kL];                      // delta_t exp(l_128 - l_t)
     float total, pad[3];
 };
 constexpr uint32_t kOffBar = kOffDec + kDecs * sizeof(Decays128);
 struct Bars {
-    uint64_t full[2], empty[2], dec_full[kDecs], dec_empty[kDecs], xw_full[2], xw_empty[2];
-    uint64_t d3_full, d3_empty, g_full, m_full, s_full, d1_full, d2_full, d_empty, fin;
+    uint64_t full[3], empty[3], dec_full[kDecs], dec_empty[kDecs], xw_full[4], xw_empty[4];
+    uint64_t d3_full[2], d3_empty[2], g_full, m_full, s_full, d1_full, d2_full, d_empty, fin;
     uint32_t tmem;
 };
 constexpr uint32_t kTcSmem = kOffBar + sizeof(Bars) + 1024;  // + alignment of the tiles
@@ -163,42 +168,36 @@ struct TcArgs {
 // Warp: the decays of a chunk from the raw dt of tokens 4 lane .. 4 lane + 3.
 __device__ __forceinline__ void chunk_decays128(Decays128& d, const float (&dt)[4], int n, float A, float bias,
                                                 bool softplus, int lane) {
-    constexpr double kLog2e = 1.4426950408889634074;
-    const double s = static_cast<double>(A) * kLog2e;
+    const Pair rate = log2_rate(A);
     float e[4];
-    double l[4], run = 0.0;
+    Pair l[4], run{0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         e[i] = dt[i] + bias;
         if (softplus) e[i] = softplus_f32(e[i]);
         if (4 * lane + i >= n) e[i] = 0.f;
-        run += e[i] * s;
+        run = pair_add(run, pair_mul(e[i], rate));
         l[i] = run;
     }
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, run, m);
-        if (lane >= m) run += o;
-    }
-    double before = __shfl_up_sync(0xffffffffu, run, 1);
-    if (lane == 0) before = 0.0;
-    const double end = __shfl_sync(0xffffffffu, run, 31);
-    const float he = static_cast<float>(end), le = static_cast<float>(end - he);
+    run = pair_scan(run, lane);
+    Pair before{__shfl_up_sync(0xffffffffu, run.h, 1), __shfl_up_sync(0xffffffffu, run.l, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+    const Pair end{__shfl_sync(0xffffffffu, run.h, 31), __shfl_sync(0xffffffffu, run.l, 31)};
     float hi[4], lo[4], from[4], w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const double c = before + l[i];
-        hi[i] = static_cast<float>(c);
-        lo[i] = static_cast<float>(c - hi[i]);
-        from[i] = exp2_pair(hi[i], lo[i]);
-        w[i] = e[i] * exp2_diff(he, le, hi[i], lo[i]);
+        const Pair c = pair_add(before, l[i]);
+        hi[i] = c.h;
+        lo[i] = c.l;
+        from[i] = exp2_pair(c.h, c.l);
+        w[i] = e[i] * exp2_diff(end.h, end.l, c.h, c.l);
     }
     *reinterpret_cast<float4*>(&d.delta[4 * lane]) = make_float4(e[0], e[1], e[2], e[3]);
-    *reinterpret_cast<float4*>(&d.hi[4 * lane]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<float4*>(&d.lo[4 * lane]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<float4*>(&d.hi[4 * lane]) = make_float4(-hi[0], -hi[1], -hi[2], -hi[3]);
+    *reinterpret_cast<float4*>(&d.lo[4 * lane]) = make_float4(-lo[0], -lo[1], -lo[2], -lo[3]);
     *reinterpret_cast<float4*>(&d.from[4 * lane]) = make_float4(from[0], from[1], from[2], from[3]);
     *reinterpret_cast<float4*>(&d.w[4 * lane]) = make_float4(w[0], w[1], w[2], w[3]);
-    if (lane == 31) d.total = exp2_pair(he, le);
+    if (lane == 31) d.total = exp2_pair(end.h, end.l);
 }
 
 // OUT, whole: as in scan_kernel (wkv7_scan.cu).
@@ -215,6 +214,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int h = blockIdx.x % a.H, grp = h / (a.H / a.G);
     const long slot = blockIdx.x / a.H;
     constexpr long kState = static_cast<long>(kScanP) * kN;
+    // the pass over states loads less and keeps less: deeper rings
+    constexpr int kStages = OUT ? 2 : 3, kRing = OUT ? 2 : 4, kD3s = OUT ? 1 : 2;
+    constexpr uint32_t kStageBytes = OUT ? kStage : 3 * kTile;
+    static_assert(kStages * kStageBytes <= kOffS, "the stages");
+    constexpr uint32_t kXw = OUT ? kOffXw : kOffXwStates;
 
     int n;
     long r0, r1, lo, hi;
@@ -232,18 +236,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp == kWarpMma) {
         if (lane == 0) {
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < kStages; ++i) {
                 mbar_init(&bar.full[i], 1);
                 mbar_init(&bar.empty[i], OUT ? 9 : 1);
+            }
+            for (int i = 0; i < kD3s; ++i) {
+                mbar_init(&bar.d3_full[i], 1);
+                mbar_init(&bar.d3_empty[i], 8);
+            }
+            for (int i = 0; i < kRing; ++i) {
                 mbar_init(&bar.xw_full[i], 4);
                 mbar_init(&bar.xw_empty[i], 1);
             }
             for (int i = 0; i < kDecs; ++i) {
                 mbar_init(&bar.dec_full[i], 1);
-                mbar_init(&bar.dec_empty[i], OUT ? 20 : 12);
+                mbar_init(&bar.dec_empty[i], 20);  // every warp of M, S and x
             }
-            mbar_init(&bar.d3_full, 1);
-            mbar_init(&bar.d3_empty, 8);
             mbar_init(&bar.g_full, 1);
             mbar_init(&bar.m_full, 8);
             mbar_init(&bar.s_full, 8);
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) arrive(&b);
     };
 
-    if (warp < kWarpS) {
+    if (OUT && warp < kWarpS) {
         // ------------------------------------------------------------ M from G
         if constexpr (OUT) {
             const int q = warp & 3, half = warp >> 2;
@@ -295,7 +303,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const Decays128& d = dec[c % kDecs];
-                const float ht = d.hi[t], lt = d.lo[t];
+                // the columns' parts are stored negated
+                const float2 ht = make_float2(-d.hi[t], -d.hi[t]), lt = make_float2(-d.lo[t], -d.lo[t]);
                 // pieces of 16 columns: two to a block of 32, blocks half, half + 2 up to q
                 const int pieces = q >= half ? 2 * ((q - half) / 2 + 1) : 0;
                 auto col = [&](int i) { return 32 * (half + 2 * (i >> 1)) + 16 * (i & 1); };
@@ -317,10 +326,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const float4 ls = *reinterpret_cast<const float4*>(&d.lo[s]);
                         const float4 ds = *reinterpret_cast<const float4*>(&d.delta[s]);
                         float m[4];
-                        m[0] = g[k] * (ex2_ftz((ht - hs.x) + (lt - ls.x)) * ds.x);
-                        m[1] = g[k + 1] * (ex2_ftz((ht - hs.y) + (lt - ls.y)) * ds.y);
-                        m[2] = g[k + 2] * (ex2_ftz((ht - hs.z) + (lt - ls.z)) * ds.z);
-                        m[3] = g[k + 3] * (ex2_ftz((ht - hs.w) + (lt - ls.w)) * ds.w);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 x = add2(add2(ht, e ? make_float2(hs.z, hs.w) : make_float2(hs.x, hs.y)),
+                                                  add2(lt, e ? make_float2(ls.z, ls.w) : make_float2(ls.x, ls.y)));
+                            const float2 v = mul2(mul2(make_float2(ex2_ftz(x.x), ex2_ftz(x.y)),
+                                                       e ? make_float2(ds.z, ds.w) : make_float2(ds.x, ds.y)),
+                                                  make_float2(g[k + e], g[k + e + 1]));
+                            m[e] = v.x, m[e + 1] = v.y;
+                        }
                         if (s0 + 16 > 32 * q) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) m[e] = s + e <= t ? m[e] : 0.f;
@@ -340,7 +354,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 signal(bar.dec_empty[c % kDecs]);
             }
         }
-    } else if (warp < kWarpX) {
+    } else if (warp >= kWarpS && warp < kWarpX) {
         // ------------------------------------------------------------ the state and y
         const int row = 32 * (warp & 3) + lane;       // column n of the state; token t of y
         const int p0 = warp >= kWarpS + 4 ? kHalf : 0;  // this warp's rows p of the state and channels of y
@@ -370,24 +384,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int c = 0; c < chunks && ok; ++c) {
             const Decays128& d = dec[c % kDecs];
             wait(bar.dec_full[c % kDecs], c / kDecs);
-            wait(bar.d3_full, c);
+            wait(bar.d3_full[c % kD3s], c / kD3s);
             if (!ok) break;
             tc_fence_after();
             const float tot = d.total, f = d.from[row];
             signal(bar.dec_empty[c % kDecs]);
             run *= tot;
             {
+                const uint32_t d3 = tm + lane_base + kColD3 - (c % kD3s) * 64;
                 float v[2][16];
                 __syncwarp();
-                tmem_load16(tm + lane_base + kColD3 + p0, v[0]);
-                tmem_load16(tm + lane_base + kColD3 + p0 + 16, v[1]);
+                tmem_load16(d3 + p0, v[0]);
+                tmem_load16(d3 + p0 + 16, v[1]);
                 tmem_wait(v[0]);
                 tmem_wait(v[1]);
 #pragma unroll
-                for (int e = 0; e < kHalf; ++e) S[e] = fmaf(tot, S[e], v[e / 16][e % 16]);
+                for (int e = 0; e < kHalf; e += 2) {
+                    const float2 r = fma2(make_float2(tot, tot), make_float2(S[e], S[e + 1]),
+                                          make_float2(v[e / 16][e % 16], v[e / 16][e % 16 + 1]));
+                    S[e] = r.x, S[e + 1] = r.y;
+                }
             }
             tc_fence_before();
-            signal(bar.d3_empty);
+            signal(bar.d3_empty[c % kD3s]);
             if constexpr (OUT) {
                 wait(bar.d1_full, c);  // (2) has read the planes
                 if (!ok) break;
@@ -395,7 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 wait(bar.d2_full, c);
                 if (!ok) break;
                 tc_fence_after();
-                const uint8_t* xs = sm + (c & 1) * kStage;
+                const uint8_t* xs = sm + (c % kStages) * kStageBytes;
                 __nv_bfloat16* dst = a.y + (r0 + static_cast<long>(c) * kL + row) * a.ldy + h * kScanP + p0;
                 const bool live = row < count(c);
 #pragma unroll 1
@@ -411,7 +430,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tmem_wait(w);
                         tmem_wait(v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) u[e] += w[e];
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 r = fma2(make_float2(f, f),
+                                                  add2(make_float2(u[e], u[e + 1]), make_float2(w[e], w[e + 1])),
+                                                  make_float2(v[e], v[e + 1]));
+                            u[e] = r.x, u[e + 1] = r.y;
+                        }
                     }
                     if (i == kHalf - 16) {
                         tc_fence_before();
@@ -423,13 +447,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
                         uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[e] = pack_bf16(fmaf(Dh, bf_lo(xw[e]), fmaf(f, u[k + 2 * e], v[k + 2 * e])),
-                                             fmaf(Dh, bf_hi(xw[e]), fmaf(f, u[k + 2 * e + 1], v[k + 2 * e + 1])));
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 r = fma2(make_float2(Dh, Dh), make_float2(bf_lo(xw[e]), bf_hi(xw[e])),
+                                                  make_float2(u[k + 2 * e], u[k + 2 * e + 1]));
+                            o[e] = pack_bf16(r.x, r.y);
+                        }
                         if (live) *reinterpret_cast<uint4*>(dst + i + k) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
-                signal(bar.empty[c & 1]);
+                signal(bar.empty[c % kStages]);
             }
         }
         float* dst = whole ? (a.sT ? a.sT + seq_state : nullptr) : OUT ? nullptr : a.seg_state + slot_state;
@@ -438,60 +464,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int p = 0; p < kHalf; ++p) dst[(p0 + p) * kN + row] = S[p];
         }
         if (!OUT && !whole && warp == kWarpS && lane == 0) a.seg_decay[slot * a.H + h] = run;
-    } else if (warp < kWarpLoad) {
+    } else if (warp < kWarpMma && warp != kWarpLoad) {
         // ------------------------------------------------------------ the scaled x
-        const int w = tid - kWarpX * 32, r = w >> 2, part = (w & 3) * 32;  // row of a piece; bytes part .. of it
-        for (int c = 0; c < chunks && ok; ++c) {
+        // One group of four warps; without outputs the warps of M are two more, and the
+        // groups take the pieces in turn.
+        const int group = warp < kWarpS ? 1 + (warp >> 2) : 0, groups = OUT ? 1 : 3;
+        const int w = (warp < kWarpS ? warp & 3 : warp == 20 ? 3 : warp - kWarpX) * 32 + lane;
+        const int r = w >> 2, part = (w & 3) * 32;  // row of a piece; bytes part .. of it
+        int now = -1;                               // the chunk at hand
+        for (int piece = group; piece < 4 * chunks && ok; piece += groups) {
+            const int c = piece >> 2, s = 32 * (piece & 3) + r, ring = piece % kRing;
             const Decays128& d = dec[c % kDecs];
-            const int nr = count(c);
-            uint8_t* st = sm + (c & 1) * kStage;
-            wait(bar.full[c & 1], c >> 1);
-            wait(bar.dec_full[c % kDecs], c / kDecs);
-#pragma unroll 1
-            for (int k = 0; k < 4 && ok; ++k) {
-                const int piece = 4 * c + k, s = 32 * k + r;
-                if (piece >= 2) wait(bar.xw_empty[piece & 1], (piece >> 1) - 1);
-                if (!ok) break;
-                const bool live = s < nr;
-                const float f = d.w[s];
-                uint8_t* out = sm + kOffXw + (piece & 1) * 3 * kPiece;
-#pragma unroll
-                for (int b = 0; b < 32; b += 16) {
-                    const uint4 xv = *reinterpret_cast<const uint4*>(st + swz(s, part + b, kL));
-                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-                    uint32_t u[4][3];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        split_pair<3>(u[e], live ? f * bf_lo(xw[e]) : 0.f, live ? f * bf_hi(xw[e]) : 0.f);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        *reinterpret_cast<uint4*>(out + p * kPiece + swz(r, part + b, 32)) =
-                            make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
-                    if (!live) {
-                        // Rows of the next sequence: their x and B meet factors of zero in (3) and (4),
-                        // which an infinity or NaN would not survive.
-                        const uint4 z = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(st + swz(s, part + b, kL)) = z;
-                        *reinterpret_cast<uint4*>(st + kTile + swz(s, part + b, kL)) = z;
-                        *reinterpret_cast<uint4*>(st + 2 * kTile + swz(s, part + b, kL)) = z;
-                    }
-                }
-                fence_proxy_async_smem();
-                signal(bar.xw_full[piece & 1]);
+            uint8_t* st = sm + (c % kStages) * kStageBytes;
+            if (c != now) {
+                for (; now < c; ++now)
+                    if (now >= 0) signal(bar.dec_empty[now % kDecs]);
+                wait(bar.full[c % kStages], c / kStages);
+                wait(bar.dec_full[c % kDecs], c / kDecs);
             }
-            signal(bar.dec_empty[c % kDecs]);
+            if (piece >= kRing) wait(bar.xw_empty[ring], piece / kRing - 1);
+            if (!ok) break;
+            const bool live = s < count(c);
+            const float f = d.w[s];
+            uint8_t* out = sm + kXw + ring * 3 * kPiece;
+#pragma unroll
+            for (int b = 0; b < 32; b += 16) {
+                uint4 xv = *reinterpret_cast<const uint4*>(st + swz(s, part + b, kL));
+                if (!live) {
+                    // Rows of the next sequence: their x and B meet factors of zero in (3) and (4),
+                    // which an infinity or NaN would not survive.
+                    xv = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(st + swz(s, part + b, kL)) = xv;
+                    *reinterpret_cast<uint4*>(st + kTile + swz(s, part + b, kL)) = xv;
+                    *reinterpret_cast<uint4*>(st + 2 * kTile + swz(s, part + b, kL)) = xv;
+                }
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t u[4][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = mul2(make_float2(f, f), make_float2(bf_lo(xw[e]), bf_hi(xw[e])));
+                    split_pair<3>(u[e], v.x, v.y);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    *reinterpret_cast<uint4*>(out + p * kPiece + swz(r, part + b, 32)) =
+                        make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
+            }
+            fence_proxy_async_smem();
+            signal(bar.xw_full[ring]);
         }
+        for (; ok && now < chunks; ++now)
+            if (now >= 0) signal(bar.dec_empty[now % kDecs]);
     } else if (warp == kWarpLoad) {
         // ------------------------------------------------------------ loads
         int issued = 0;
         for (int c = 0; c < chunks && ok; ++c) {
-            const int st = c & 1;
-            if (c >= 2) wait(bar.empty[st], (c >> 1) - 1);
+            const int st = c % kStages;
+            if (c >= kStages) wait(bar.empty[st], c / kStages - 1);
             if (!ok) break;
             if (lane == 0) {
-                uint8_t* p = sm + st * kStage;
+                uint8_t* p = sm + st * kStageBytes;
                 const int row = static_cast<int>(r0 + static_cast<long>(c) * kL);
-                mbar_arrive_expect_tx(&bar.full[st], OUT ? kStage : 3 * kTile);
+                mbar_arrive_expect_tx(&bar.full[st], kStageBytes);
                 tma_load_2d(p + kTile, &maps.b, &bar.full[st], grp * kN, row);
                 tma_load_2d(p + 2 * kTile, &maps.b, &bar.full[st], grp * kN + 64, row);
                 if constexpr (OUT) {
@@ -505,8 +539,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // nothing may still be on its way into shared memory when the block ends
         if (!ok)
-            for (int c = issued < 2 ? 0 : issued - 2; c < issued; ++c)
-                mbar_wait(&bar.full[c & 1], static_cast<uint32_t>(c >> 1) & 1u, 2000000000ull);
+            for (int c = issued < kStages ? 0 : issued - kStages; c < issued; ++c)
+                mbar_wait(&bar.full[c % kStages], static_cast<uint32_t>(c / kStages) & 1u, 2000000000ull);
     } else if (warp >= kWarpDec) {
         // ------------------------------------------------------------ decays
         const float Ah = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
@@ -529,9 +563,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else {
         // ------------------------------------------------------------ products
         const uint64_t dX = desc_mn(sb, kTile), dBk = desc_k(sb + kTile), dBn = desc_mn(sb + kTile, kTile),
-                       dC = desc_k(sb + 3 * kTile), dS = desc_mn(sb + kOffS, kTile), dXw = desc_mn(sb + kOffXw, kPiece);
+                       dC = desc_k(sb + 3 * kTile), dS = desc_mn(sb + kOffS, kTile), dXw = desc_mn(sb + kXw, kPiece);
         auto products_g = [&](int c) {
-            const uint64_t st = (c & 1) * at(kStage);
+            const uint64_t st = (c % kStages) * at(kStageBytes);
             if (elect_one()) {
                 uint64_t p = dC + st, q = dBk + st;
 #pragma unroll 1
@@ -546,31 +580,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         };
         for (int c = 0; c < chunks && ok; ++c) {
-            const int st = c & 1;
-            const uint64_t so = st * at(kStage);
+            const int st = c % kStages;
+            const uint64_t so = st * at(kStageBytes);
+            const uint32_t d3 = tm + kColD3 - (c % kD3s) * 64;
             if (!OUT || c == 0) {
-                wait(bar.full[st], c >> 1);
+                wait(bar.full[st], c / kStages);
                 if (!ok) break;
                 tc_fence_after();
                 if constexpr (OUT) products_g(0);
             }
             // (4), half of its pieces at a time: the ring is filled again while (2) runs
-            if (c > 0) wait(bar.d3_empty, c - 1);
+            if (c >= kD3s) wait(bar.d3_empty[c % kD3s], c / kD3s - 1);
             auto products_s = [&](int k) {
-                wait(bar.xw_full[k & 1], (4 * c + k) >> 1);
+                const int ring = k % kRing;
+                wait(bar.xw_full[ring], (4 * c + k) / kRing);
                 if (!ok) return;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t p = dBn + so + step_mn(2 * k);
-                    uint64_t q = dXw + (k & 1) * at(3 * kPiece);
+                    uint64_t q = dXw + ring * at(3 * kPiece);
 #pragma unroll 1
                     for (int i = 0; i < 3; ++i, q += at(kPiece)) {
-                        mma_smem(tm + kColD3, p, q, kIdS, k > 0 || i > 0);
-                        mma_smem(tm + kColD3, p + step_mn(1), q + step_mn(1), kIdS, true);
+                        mma_smem(d3, p, q, kIdS, k > 0 || i > 0);
+                        mma_smem(d3, p + step_mn(1), q + step_mn(1), kIdS, true);
                     }
-                    mma_commit(&bar.xw_empty[k & 1]);
+                    mma_commit(&bar.xw_empty[ring]);
                     if (k == 3) {
-                        mma_commit(&bar.d3_full);
+                        mma_commit(&bar.d3_full[c % kD3s]);
                         if constexpr (!OUT) mma_commit(&bar.empty[st]);
                     }
                 }
@@ -620,7 +656,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 // (1) of the next chunk: M of this one has been made, so G is free
                 if (c + 1 < chunks) {
-                    wait(bar.full[st ^ 1], (c + 1) >> 1);
+                    wait(bar.full[(c + 1) % kStages], (c + 1) / kStages);
                     if (!ok) break;
                     tc_fence_after();
                     products_g(c + 1);
