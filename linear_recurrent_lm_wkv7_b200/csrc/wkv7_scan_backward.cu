@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
     using TS = typename LY::TS;
     constexpr int PI = LY::PI, PC = LY::PC, NT = N / 8;
     constexpr int NB = N < 32 ? N : 32;  // state columns worked on at a time
-    constexpr long kState = static_cast<long>(kScanP) * N;
+    constexpr int kState = kScanP * N;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     Decays* dec = reinterpret_cast<Decays*>(smem + LY::off_d);
@@ -559,22 +559,32 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
         {
             float dot = 0.f;
             const __nv_bfloat16* g = a.states + (slot * a.H + h0 + i) * (kStatePlanes * kState);
-            for (int p = tid; p < kState / 2; p += kScanThreads) {
-                const int r = p / (N / 2), c = p % (N / 2) * 2;
-                const float2 u = tile_pair<TS>(smem, ods, r, c);
-                float2 v;
-                if constexpr (LY::shared_state) {
-                    v = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int k = kStatePlanes - 1; k >= 0; --k) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(g + k * kState + r * N + c);
-                        v.x += bf_lo(w);
-                        v.y += bf_hi(w);
-                    }
-                } else {
-                    v = tile_pair<TS>(smem, os0, r, c);
+            for (int k = 0; k < kState / 8 / kScanThreads + (kState / 8 % kScanThreads ? 1 : 0); ++k) {
+                const int p = tid + k * kScanThreads;
+                if (kState / 8 % kScanThreads && p >= kState / 8) continue;
+                const int r = p / (N / 8), c = p % (N / 8) * 8;  // eight columns of a row
+                uint4 u[kStatePlanes], v[kStatePlanes];
+#pragma unroll
+                for (int w = 0; w < kStatePlanes; ++w) {
+                    u[w] = *reinterpret_cast<const uint4*>(smem + ods + w * TS::plane + r * TS::pitch + c * 2);
+                    if constexpr (LY::shared_state)
+                        v[w] = *reinterpret_cast<const uint4*>(g + w * kState + r * N + c);
+                    else
+                        v[w] = *reinterpret_cast<const uint4*>(smem + os0 + w * TS::plane + r * TS::pitch + c * 2);
                 }
-                dot = fmaf(u.x, v.x, fmaf(u.y, v.y, dot));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 x = make_float2(0.f, 0.f), y = x;
+#pragma unroll
+                    for (int w = kStatePlanes - 1; w >= 0; --w) {
+                        const uint32_t a1 = (&u[w].x)[e], b1 = (&v[w].x)[e];
+                        x = add2(x, make_float2(bf_lo(a1), bf_hi(a1)));
+                        y = add2(y, make_float2(bf_lo(b1), bf_hi(b1)));
+                    }
+                    const float2 z = mul2(x, y);
+                    dot += z.x + z.y;
+                }
             }
             dot = warp_sum(dot);
             if (lane == 0) hs.dot[warp] = dot;
@@ -639,24 +649,53 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             }
         }
         float sum[2] = {0.f, 0.f}, diag = 0.f;
+        {
+            // l of this lane's two rows, and pairs of columns; on the t side rows are t
+            const float sign = s_side ? -1.f : 1.f;
+            const float2 neg = make_float2(-sign, -sign);
+            float2 rh[2], rl[2], rd[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!in_tri(j >> 1)) continue;
+            for (int r = 0; r < 2; ++r) {
+                const int row = row0 + 8 * r;
+                rh[r] = make_float2(sign * d.hi[row], sign * d.hi[row]);
+                rl[r] = make_float2(sign * d.lo[row], sign * d.lo[row]);
+                rd[r] = make_float2(d.delta[row], d.delta[row]);
+            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = e >> 1, row = row0 + 8 * r, col = j * 8 + q2 + (e & 1);
-                const int t = s_side ? col : row, s = s_side ? row : col;
-                const bool keep = t >= s;
-                const float l = keep ? decay_between(d, t, s) : 0.f;
-                const float m = keep ? M[j][e] * l : 0.f;
-                const float q = m * d.delta[s];
-                Q[j][e] += q;
-                if (s_side) {
-                    sum[r] = fmaf(G[j][e], m, sum[r]);
-                    M[j][e] = G[j][e] * l;  // the weights of dy in dx
-                } else {
-                    if (t == s) diag += M[j][e];
-                    M[j][e] = t == s ? 0.f : G[j][e] * q;  // W off the diagonal, which no sum takes
+            for (int j = 0; j < 8; ++j) {
+                if (!in_tri(j >> 1)) continue;
+                const int col = j * 8 + q2;
+                const float2 ch = *reinterpret_cast<const float2*>(&d.hi[col]);
+                const float2 cl = *reinterpret_cast<const float2*>(&d.lo[col]);
+                const float2 cd = *reinterpret_cast<const float2*>(&d.delta[col]);
+                const bool edge = (j >> 1) == blk;  // the block on the diagonal
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = row0 + 8 * r;
+                    const float2 x = add2(fma2(neg, ch, rh[r]), fma2(neg, cl, rl[r]));
+                    float2 l = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+                    float2 mm = make_float2(M[j][2 * r], M[j][2 * r + 1]);
+                    const float2 g = make_float2(G[j][2 * r], G[j][2 * r + 1]);
+                    if (edge) {  // t >= s
+                        if (!s_side && row == col) diag += mm.x;
+                        if (!s_side && row == col + 1) diag += mm.y;
+                        if (s_side ? col < row : row < col) l.x = 0.f, mm.x = 0.f;
+                        if (s_side ? col + 1 < row : row < col + 1) l.y = 0.f, mm.y = 0.f;
+                    }
+                    const float2 m = mul2(mm, l);
+                    const float2 q = mul2(m, s_side ? rd[r] : cd);
+                    const float2 qs = add2(make_float2(Q[j][2 * r], Q[j][2 * r + 1]), q);
+                    Q[j][2 * r] = qs.x, Q[j][2 * r + 1] = qs.y;
+                    float2 w;
+                    if (s_side) {
+                        sum[r] = fmaf(g.x, m.x, fmaf(g.y, m.y, sum[r]));
+                        w = mul2(g, l);  // the weights of dy in dx
+                    } else {
+                        w = mul2(g, q);  // W; off the diagonal, which no sum takes
+                        if (edge && row == col) w.x = 0.f;
+                        if (edge && row == col + 1) w.y = 0.f;
+                    }
+                    M[j][2 * r] = w.x, M[j][2 * r + 1] = w.y;
                 }
             }
         }
@@ -684,25 +723,39 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
                     uint32_t ub[1][2];
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        const int s = c * 16 + w * 8 + q2, i2 = j * 8 + g8;
-                        ub[0][w] = (s < i2 ? 0x3f80u : 0u) | (s + 1 < i2 ? 0x3f800000u : 0u);
+                        const int at = (j - 2 * c) * 8 - w * 8;  // of the tile's first i behind the fragment's first s
+                        ub[0][w] = at >= 8 ? 0x3f803f80u
+                                           : at <= -8 ? 0u
+                                                      : (q2 < g8 + at ? 0x3f80u : 0u) | (q2 + 1 < g8 + at ? 0x3f800000u : 0u);
                     }
                     mma_planes<kStatePlanes, 1>(V[j], fa, ub);
                 }
             }
+            // Column sums over t >= i, lanes g8 holding rows: halves of the columns are passed on
+            // at every step, so that each lane ends with two columns' sums.
+            float v[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j > 2 * blk + 1) continue;
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i2 = j * 8 + q2 + e;
-                    float v = (row0 >= i2 ? V[j][e] : 0.f) + (row0 + 8 >= i2 ? V[j][2 + e] : 0.f);
-                    v += __shfl_xor_sync(0xffffffffu, v, 4);
-                    v += __shfl_xor_sync(0xffffffffu, v, 8);
-                    v += __shfl_xor_sync(0xffffffffu, v, 16);
-                    if (g8 == 0) hs.v[blk * kChunk + i2] = v;
+                    v[2 * j + e] = j > 2 * blk + 1 ? 0.f
+                                                   : (row0 >= i2 ? V[j][e] : 0.f) + (row0 + 8 >= i2 ? V[j][2 + e] : 0.f);
+                }
+#pragma unroll
+            for (int n2 = 8; n2 >= 2; n2 >>= 1) {  // lanes 4 n2 / 2 apart swap halves
+                const int far = 2 * n2;
+                const bool up = lane & far;
+#pragma unroll
+                for (int k = 0; k < n2; ++k) {
+                    const float give = up ? v[k] : v[n2 + k];
+                    const float got = __shfl_xor_sync(0xffffffffu, give, far);
+                    v[k] = (up ? v[n2 + k] : v[k]) + got;
                 }
             }
+            // lane bits 4, 3, 2 chose 8, 4, 2 of the 16 columns 2 j + e
+            const int k0 = ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2;
+            *reinterpret_cast<float2*>(&hs.v[blk * kChunk + (k0 / 2) * 8 + q2]) = make_float2(v[0], v[1]);
         }
 
         if (s_side) {
