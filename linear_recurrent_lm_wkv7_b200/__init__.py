@@ -304,7 +304,11 @@ def _scratch(nbytes, like):
 
 def _new(t):
     """A contiguous tensor of the shape, type and device of ``t``."""
-    return t.new_empty(t.shape)
+    global _new
+    import torch
+
+    _new = functools.partial(torch.empty_like, memory_format=torch.contiguous_format)
+    return _new(t)
 
 
 def _rows(t, seq_offsets, inner):
@@ -338,8 +342,11 @@ def causal_conv_step(x, w, state, bias=None, act=None, y=None, stream=None):
     updated in place.  Returns y ([B, C])."""
     C, W = w.shape
     if y is None:
-        with _outputs(x, stream, (x, w, state, bias)):
+        if stream is None:
             y = _new(x)
+        else:
+            with _outputs(x, stream, (x, w, state, bias)):
+                y = _new(x)
     wkv7_causal_conv_step(x, w, bias, state, y, state, x.shape[0], C, W, act, stream)
     return y
 
@@ -388,10 +395,13 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, dt_softpl
     and ``Cm`` [B, G, N], ``state`` [B, H, 64, N] fp32 updated in place.  Returns y
     ([B, H, 64])."""
     B, H, P = x.shape
-    G, N = Bm.shape[-2:]
+    _, G, N = Bm.shape
     if y is None:
-        with _outputs(x, stream, (x, dt, A, Bm, Cm, state, D, dt_bias)):
+        if stream is None:
             y = _new(x)
+        else:
+            with _outputs(x, stream, (x, dt, A, Bm, Cm, state, D, dt_bias)):
+                y = _new(x)
     wkv7_selective_scan_step(x, dt, A, Bm, Cm, D, dt_bias, state, y, state, B, H, P, N, G, dt_softplus, stream)
     return y
 

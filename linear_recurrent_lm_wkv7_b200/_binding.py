@@ -297,7 +297,7 @@ class _Runtime:
         self.f32, self.i32 = torch.float32, torch.int32
         self.codes = {torch.float32: WKV7_F32, torch.bfloat16: WKV7_BF16}
         self.device = torch.cuda.device
-        self.current_device = torch.cuda.current_device
+        self.current_device = torch._C._cuda_getDevice  # CUDA is set up: a tensor is on it
         self.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -375,6 +375,10 @@ def _rows(t, name, dtype, shape, lead, width, dev):
     """The pointer and the row stride of rows of ``width`` elements."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _wrong(t, name, dtype, shape, dev)
+    if lead == 1 and shape[0] > 1:  # the usual slice of a step or of packed rows
+        st = t.stride()
+        if st[-1] == 1 and (len(st) == 2 or st[1] == shape[2]):
+            return t.data_ptr(), st[0]
     return t.data_ptr(), _row_ld(t, lead, width, name)
 
 
@@ -389,14 +393,17 @@ def _space(t, dev):
 
 def _dev(t):
     """The ordinal of the device that a call runs on."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    return t.get_device()
+    if _RT is None:
+        _runtime()
+    return dev
 
 
 def _call(dev, stream, fn, args, where):
     """Calls the library with device ``dev`` current and raises on a status."""
-    rt = _runtime()
+    rt = _RT
     if stream is None:
         stream = rt.raw_stream(dev)
     elif hasattr(stream, "cuda_stream"):
@@ -406,14 +413,15 @@ def _call(dev, stream, fn, args, where):
     else:
         with rt.device(dev):
             st = fn(*args, stream)
-    if st != 0:
+    if st:
         raise Wkv7Error(st, where)
 
 
 def wkv7_causal_conv(x, w, bias, s0, y, sT, B, T, C, W, seq_offsets=None, act=None, stream=None):
     """Enqueue the causal convolution (see include/wkv7.h).  x and y may be slices of
     wider rows."""
-    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    dev, io, code = _dev(x), x.dtype, _code(x)
+    f32 = _RT.f32
     lead = (B, T) if seq_offsets is None else (T,)
     px, ldx = _rows(x, "x", io, lead + (C,), len(lead), C, dev)
     py, ldy = _rows(y, "y", io, lead + (C,), len(lead), C, dev)
@@ -425,13 +433,16 @@ def wkv7_causal_conv(x, w, bias, s0, y, sT, B, T, C, W, seq_offsets=None, act=No
 
 def wkv7_causal_conv_step(x, w, bias, s_in, y, s_out, B, C, W, act=None, stream=None):
     """Enqueue one token per sequence of the causal convolution (see include/wkv7.h)."""
-    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
-    px, ldx = _rows(x, "x", io, (B, C), 1, C, dev)
-    py, ldy = _rows(y, "y", io, (B, C), 1, C, dev)
+    dev, io, code = _dev(x), x.dtype, _code(x)
+    f32 = _RT.f32
+    shape, st = (B, C), (B, W - 1, C)
+    px, ldx = _rows(x, "x", io, shape, 1, C, dev)
+    py, ldy = _rows(y, "y", io, shape, 1, C, dev)
+    ps = _flat(s_in, "s_in", io, st, dev)
+    pt = ps if s_out is s_in else _flat(s_out, "s_out", io, st, dev)
     _call(dev, stream, _lib().wkv7_causal_conv_step,
           (px, ldx, _flat(w, "w", f32, (C, W), dev), _flat(bias, "bias", f32, (C,), dev),
-           _flat(s_in, "s_in", io, (B, W - 1, C), dev), py, ldy, _flat(s_out, "s_out", io, (B, W - 1, C), dev), B, C,
-           W, _act(act), code), "wkv7_causal_conv_step")
+           ps, py, ldy, pt, B, C, W, _act(act), code), "wkv7_causal_conv_step")
 
 
 def wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, packed) -> int:
@@ -441,7 +452,8 @@ def wkv7_causal_conv_backward_workspace_bytes(B, T, C, W, packed) -> int:
 def wkv7_causal_conv_backward(x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, workspace, B, T, C, W, seq_offsets=None,
                               act=None, stream=None):
     """Enqueue the gradient of the causal convolution (see include/wkv7.h)."""
-    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    dev, io, code = _dev(x), x.dtype, _code(x)
+    f32 = _RT.f32
     lead = (B, T) if seq_offsets is None else (T,)
     k, shape, st = len(lead), lead + (C,), (B, W - 1, C)
     px, ldx = _rows(x, "x", io, shape, k, C, dev)
@@ -458,13 +470,13 @@ def wkv7_causal_conv_backward(x, w, bias, s0, dy, dsT, dx, dw, dbias, ds0, works
 
 def _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, lead, H, D, N, G, dev):
     """The leading arguments that the scan's calls share: x to dt_bias."""
-    f32, io, k = _RT.f32, x.dtype, len(lead)
+    f32, io, k, hs, bs = _RT.f32, x.dtype, len(lead), (H,), lead + (G, N)
     px, ldx = _rows(x, "x", io, lead + (H, D), k, H * D, dev)
-    pt, ldt = _rows(dt, "dt", dt.dtype, lead + (H,), k, H, dev)
-    pb, ldb = _rows(Bm, "Bm", io, lead + (G, N), k, G * N, dev)
-    pc, ldc = _rows(Cm, "Cm", io, lead + (G, N), k, G * N, dev)
-    return (px, ldx, pt, ldt, _flat(A, "A", f32, (H,), dev), pb, ldb, pc, ldc,
-            _flat(D_skip, "D_skip", f32, (H,), dev), _flat(dt_bias, "dt_bias", f32, (H,), dev))
+    pt, ldt = _rows(dt, "dt", dt.dtype, lead + hs, k, H, dev)
+    pb, ldb = _rows(Bm, "Bm", io, bs, k, G * N, dev)
+    pc, ldc = _rows(Cm, "Cm", io, bs, k, G * N, dev)
+    return (px, ldx, pt, ldt, _flat(A, "A", f32, hs, dev), pb, ldb, pc, ldc, _flat(D_skip, "D_skip", f32, hs, dev),
+            _flat(dt_bias, "dt_bias", f32, hs, dev))
 
 
 def wkv7_selective_scan_workspace_bytes(B, T, H, D, N, packed) -> int:
@@ -475,7 +487,8 @@ def wkv7_selective_scan(x, dt, A, Bm, Cm, D_skip, dt_bias, s0, y, sT, workspace,
                         dt_softplus=True, stream=None):
     """Enqueue the selective scan (see include/wkv7.h).  x, dt, Bm, Cm and y may be
     slices of wider rows."""
-    f32, dev, code, dtc = _runtime().f32, _dev(x), _code(x), _code(dt)
+    dev, code, dtc = _dev(x), _code(x), _code(dt)
+    f32 = _RT.f32
     lead = (B, T) if seq_offsets is None else (T,)
     ins = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, lead, H, D, N, G, dev)
     ws, nbytes = _space(workspace, dev)
@@ -490,11 +503,13 @@ def wkv7_selective_scan(x, dt, A, Bm, Cm, D_skip, dt_bias, s0, y, sT, workspace,
 def wkv7_selective_scan_step(x, dt, A, Bm, Cm, D_skip, dt_bias, s_in, y, s_out, B, H, D, N, G, dt_softplus=True,
                              stream=None):
     """Enqueue one token per sequence of the selective scan (see include/wkv7.h)."""
-    f32, dev, code, dtc = _runtime().f32, _dev(x), _code(x), _code(dt)
+    dev, code, dtc = _dev(x), _code(x), _code(dt)
+    st = (B, H, D, N)
+    ps = _flat(s_in, "s_in", _RT.f32, st, dev)
+    pt = ps if s_out is s_in else _flat(s_out, "s_out", _RT.f32, st, dev)
     _call(dev, stream, _lib().wkv7_selective_scan_step,
-          _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, (B,), H, D, N, G, dev) +
-          (_flat(s_in, "s_in", f32, (B, H, D, N), dev),) + _rows(y, "y", x.dtype, (B, H, D), 1, H * D, dev) +
-          (_flat(s_out, "s_out", f32, (B, H, D, N), dev), B, H, D, N, G, 1 if dt_softplus else 0, code, dtc),
+          (*_scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, (B,), H, D, N, G, dev), ps,
+           *_rows(y, "y", x.dtype, (B, H, D), 1, H * D, dev), pt, B, H, D, N, G, 1 if dt_softplus else 0, code, dtc),
           "wkv7_selective_scan_step")
 
 
@@ -506,7 +521,8 @@ def wkv7_selective_scan_backward(x, dt, A, Bm, Cm, D_skip, dt_bias, s0, dy, dsT,
                                  ds0, workspace, B, T, H, D, N, G, seq_offsets=None, dt_softplus=True, stream=None):
     """Enqueue the gradient of the selective scan (see include/wkv7.h).  dx, dB and dC may
     be column slices of one buffer, for the convolution's backward to take."""
-    f32, dev, code, dtc = _runtime().f32, _dev(x), _code(x), _code(dt)
+    dev, code, dtc = _dev(x), _code(x), _code(dt)
+    f32 = _RT.f32
     lead = (B, T) if seq_offsets is None else (T,)
     k, io, st = len(lead), x.dtype, (B, H, D, N)
     ins = _scan_inputs(x, dt, A, Bm, Cm, D_skip, dt_bias, lead, H, D, N, G, dev)
@@ -532,7 +548,8 @@ def wkv7_group_norm_workspace_bytes(N, L, C, G, io_dtype) -> int:
 
 def wkv7_group_norm(x, weight, bias, y, stats, workspace, N, L, C, G, eps=1e-5, act=None, stream=None):
     """Enqueue the group norm (see include/wkv7.h)."""
-    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    dev, io, code = _dev(x), x.dtype, _code(x)
+    f32 = _RT.f32
     lead = _norm_lead(x, N, L)
     px, ldx = _rows(x, "x", io, lead + (C,), len(lead), C, dev)
     py, ldy = _rows(y, "y", io, lead + (C,), len(lead), C, dev)
@@ -550,7 +567,8 @@ def wkv7_group_norm_backward_workspace_bytes(N, L, C, G, io_dtype) -> int:
 def wkv7_group_norm_backward(x, weight, bias, stats, dy, dx, dweight, dbias, workspace, N, L, C, G, act=None,
                              stream=None):
     """Enqueue the gradient of the group norm (see include/wkv7.h)."""
-    f32, dev, io, code = _runtime().f32, _dev(x), x.dtype, _code(x)
+    dev, io, code = _dev(x), x.dtype, _code(x)
+    f32 = _RT.f32
     lead = _norm_lead(x, N, L)
     k, shape = len(lead), lead + (C,)
     px, ldx = _rows(x, "x", io, shape, k, C, dev)

@@ -114,8 +114,8 @@ int wkv7_causal_conv(const void* x, int64_t ld_x, const float* w, const float* b
         return WKV7_ERR_INVALID_ARG;
     if ((s = wkv7::device_check()) != WKV7_OK) return s;
     if (T == 0 && !sT) return WKV7_OK;
-    int* status = nullptr;
-    if (wkv7::device_status_word(&status) != WKV7_OK) return WKV7_ERR_CUDA;
+    int* status = nullptr;  // dense batches have nothing to report
+    if (seq_offsets && wkv7::device_status_word(&status) != WKV7_OK) return WKV7_ERR_CUDA;
     const wkv7::ConvArgs p{x, ld_x, w, bias, s0, y, ld_y, sT, B, T, C, W, seq_offsets, act, status};
     return done(wkv7::launch_conv(p, io_dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -166,7 +166,7 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
         return WKV7_ERR_INVALID_ARG;
     if ((s = wkv7::device_check()) != WKV7_OK) return s;
     int* status = nullptr;
-    if (wkv7::device_status_word(&status) != WKV7_OK) return WKV7_ERR_CUDA;
+    if (seq_offsets && wkv7::device_status_word(&status) != WKV7_OK) return WKV7_ERR_CUDA;
     const wkv7::ConvBwdArgs p{x,     ld_x, w,   bias,  s0,  dy, ld_dy, dsT, dx, ld_dx, dw,
                               dbias, ds0,  static_cast<float*>(workspace), B, T, C, W, seq_offsets, act, status};
     return done(wkv7::launch_conv_backward(p, io_dtype, static_cast<cudaStream_t>(stream)));
