@@ -445,8 +445,6 @@ int wkv7_selective_scan_backward(const void* x, int64_t ld_x, const void* dt, in
  * wkv7_group_norm_backward: the gradient of <dy, y>; stats as the forward wrote them;
  * dx : rows of C;  dweight, dbias : [C] or NULL (zeros when there are no rows).  Sums
  * are taken in a fixed order.  workspace : wkv7_group_norm_backward_workspace_bytes.
- * Samples are numbered in 16 bits where a group does not fit one block (L > 1, or
- * more than 1024 vectors of channels in a row's group): N <= 65535 there.
  */
 size_t wkv7_group_norm_workspace_bytes(int N, int L, int C, int G, int io_dtype);
 int wkv7_group_norm(const void* x, int64_t ld_x, const float* weight, const float* bias, void* y, int64_t ld_y,

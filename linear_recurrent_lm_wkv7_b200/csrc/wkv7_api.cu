@@ -83,7 +83,7 @@ cudaError_t launch_copy_states(const float* s0, float* sT, long n, cudaStream_t 
 
 extern "C" {
 
-int wkv7_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+int wkv7_version(void) { return 1 * 10000 + 1 * 100 + 0; }
 
 const char* wkv7_status_string(int status) {
     switch (status) {

@@ -266,19 +266,19 @@ __device__ __forceinline__ Moments merge(const Moments& a, const Moments& b) {
     return {n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
 }
 
-// Block (split, sample, tile of 256 vectors of channels).  Thread: one vector, every
+// Block (sample and split, tile of 256 vectors of channels).  Thread: one vector, every
 // `par`-th row of the split.
 template <typename IO, int VEC>
 __global__ void __launch_bounds__(kThreads)
     norm_stats_kernel(const IO* __restrict__ x, long ldx, float* __restrict__ part, long L, int C, int Cg, int lanes,
-                      long split_rows) {
+                      int splits, long split_rows) {
     __shared__ Moments mom[kThreads];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
-    const int c0 = blockIdx.z * lanes * VEC, c = c0 + lane * VEC;
+    const int c0 = blockIdx.y * lanes * VEC, c = c0 + lane * VEC;
     const bool member = prow < par && c < C;
-    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l0 = static_cast<long>(blockIdx.x % splits) * split_rows;
     const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
-    const IO* base = x + static_cast<long>(blockIdx.y) * L * ldx + c;
+    const IO* base = x + static_cast<long>(blockIdx.x / splits) * L * ldx + c;
     // sums about the first value of the thread: exact enough unless that value lies many
     // deviations off, and then it dominates the deviation itself
     float pivot = 0.f, s = 0.f, ss = 0.f;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (ln == 0) {
             // [sample][group][tile][split]: what one group is joined from lies together
-            float* p = part + (((static_cast<long>(blockIdx.y) * G + g) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) * 3;
+            float* p = part + (((static_cast<long>(blockIdx.x / splits) * G + g) * gridDim.y + blockIdx.y) * splits + blockIdx.x % splits) * 3;
             p[0] = t.n, p[1] = t.mean, p[2] = t.m2;
         }
     }
@@ -378,24 +378,24 @@ template <typename IO, int VEC, bool JOIN>
 __global__ void __launch_bounds__(kThreads)
     norm_apply_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
                       const float* __restrict__ bias, float* __restrict__ stats, IO* __restrict__ y, long ldy, long L,
-                      int C, int Cg, int lanes, long split_rows, int act, const float* __restrict__ part, float eps) {
+                      int C, int Cg, int lanes, int splits, long split_rows, int act, const float* __restrict__ part, float eps) {
     __shared__ float2 joined[JOIN ? kThreads * VEC : 1];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
-    const int c0 = blockIdx.z * lanes * VEC, c = c0 + lane * VEC, G = C / Cg;
-    const long n = blockIdx.y;
+    const int c0 = blockIdx.y * lanes * VEC, c = c0 + lane * VEC, G = C / Cg;
+    const long n = blockIdx.x / splits;
     if constexpr (JOIN) {
         const int cend = min(c0 + lanes * VEC, C), g0 = c0 / Cg;
         for (int g = g0 + threadIdx.x / 32; g * Cg < cend; g += kThreads / 32) {
-            const float2 s = join_moments(part, n, g, G, Cg, gridDim.x, gridDim.z, lanes * VEC, eps, threadIdx.x % 32);
+            const float2 s = join_moments(part, n, g, G, Cg, splits, gridDim.y, lanes * VEC, eps, threadIdx.x % 32);
             if (threadIdx.x % 32 == 0) {
                 joined[g - g0] = s;
-                if (stats && blockIdx.x == 0) *reinterpret_cast<float2*>(stats + 2 * (n * G + g)) = s;
+                if (stats && blockIdx.x % splits == 0) *reinterpret_cast<float2*>(stats + 2 * (n * G + g)) = s;
             }
         }
         __syncthreads();
     }
     if (prow >= par || c >= C) return;
-    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l0 = static_cast<long>(blockIdx.x % splits) * split_rows;
     const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
     const float2 st = JOIN ? joined[c / Cg - c0 / Cg] : *reinterpret_cast<const float2*>(stats + 2 * (n * G + c / Cg));
     float wv[VEC], bv[VEC];
@@ -418,15 +418,15 @@ template <typename IO, int VEC>
 __global__ void __launch_bounds__(kThreads)
     norm_bwd_sums_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
                          const float* __restrict__ bias, const float* __restrict__ stats, const IO* __restrict__ dy,
-                         long lddy, float* __restrict__ part, long L, int C, int Cg, int lanes, long split_rows,
+                         long lddy, float* __restrict__ part, long L, int C, int Cg, int lanes, int splits, long split_rows,
                          int act) {
     __shared__ float sums[2][kThreads * VEC];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
-    const int c = (blockIdx.z * lanes + lane) * VEC;
+    const int c = (blockIdx.y * lanes + lane) * VEC;
     const bool member = prow < par && c < C;
-    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l0 = static_cast<long>(blockIdx.x % splits) * split_rows;
     const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
-    const long n = blockIdx.y;
+    const long n = blockIdx.x / splits;
     float aw[VEC], ab[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) aw[e] = ab[e] = 0.f;
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int t = 0; t < par; ++t)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[e] += sums[which][(t * lanes + lane) * VEC + e];
-        store_vec<VEC>(part + ((n * gridDim.x + blockIdx.x) * 2 + which) * C + c, s);
+        store_vec<VEC>(part + ((n * splits + blockIdx.x % splits) * 2 + which) * C + c, s);
     }
 }
 
@@ -498,13 +498,13 @@ __global__ void __launch_bounds__(kThreads)
     norm_bwd_apply_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
                           const float* __restrict__ bias, const float* __restrict__ stats,
                           const float* __restrict__ mom, const IO* __restrict__ dy, long lddy, IO* __restrict__ dx,
-                          long lddx, long L, int C, int Cg, int lanes, long split_rows, int act) {
+                          long lddx, long L, int C, int Cg, int lanes, int splits, long split_rows, int act) {
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
-    const int c = (blockIdx.z * lanes + lane) * VEC;
+    const int c = (blockIdx.y * lanes + lane) * VEC;
     if (prow >= par || c >= C) return;
-    const long l0 = static_cast<long>(blockIdx.x) * split_rows;
+    const long l0 = static_cast<long>(blockIdx.x % splits) * split_rows;
     const long l1 = l0 + split_rows < L ? l0 + split_rows : L;
-    const long n = blockIdx.y, u = n * (C / Cg) + c / Cg;
+    const long n = blockIdx.x / splits, u = n * (C / Cg) + c / Cg;
     const float mean = stats[2 * u], rstd = stats[2 * u + 1], m1 = mom[2 * u], m2 = mom[2 * u + 1];
     float wv[VEC], bv[VEC];
     load_param<VEC>(wv, weight, c, 1.f);
@@ -622,21 +622,21 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
     const Split s = split_of(p.N, p.L, p.C, VEC);
     float* part = p.ws;
     float* stats = p.stats ? p.stats : part + static_cast<size_t>(p.N) * s.splits * s.tiles * p.G * 3;
-    const dim3 grid(s.splits, p.N, s.tiles);
-    norm_stats_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, part, p.L, p.C, Cg, s.lanes, s.split_rows);
+    const dim3 grid(static_cast<unsigned>(p.N) * s.splits, s.tiles);
+    norm_stats_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, part, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows);
     // A launch less where the blocks can join the moments on the side: up to kJoinMost of
     // them each (45 groups of 132 splits, fp32 [3][2111][960]: 15.5 us against 23 with a
     // launch for the join).
     const int tile_groups = (s.lanes * VEC + Cg - 1) / Cg + 1;
     if (static_cast<long>(tile_groups) * s.splits * ((Cg + s.lanes * VEC - 1) / (s.lanes * VEC) + 1) <= kJoinMost) {
         norm_apply_kernel<IO, VEC, true><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, y, p.ldy, p.L,
-                                                                    p.C, Cg, s.lanes, s.split_rows, p.act, part,
+                                                                    p.C, Cg, s.lanes, s.splits, s.split_rows, p.act, part,
                                                                     p.eps);
     } else {
         norm_join_kernel<<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, st>>>(
             part, stats, units, p.G, Cg, s.splits, s.tiles, s.lanes * VEC, p.eps);
         norm_apply_kernel<IO, VEC, false><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, stats, y, p.ldy, p.L,
-                                                                     p.C, Cg, s.lanes, s.split_rows, p.act, nullptr,
+                                                                     p.C, Cg, s.lanes, s.splits, s.split_rows, p.act, nullptr,
                                                                      p.eps);
     }
     return cudaGetLastError();
@@ -665,14 +665,13 @@ cudaError_t norm_bwd_typed(const NormBwdArgs& p, cudaStream_t st) {
         const Split s = split_of(p.N, p.L, p.C, VEC);
         nblk = static_cast<long>(p.N) * s.splits;
         float* mom = p.ws + static_cast<size_t>(nblk) * 2 * p.C;
-        const dim3 grid(s.splits, p.N, s.tiles);
+        const dim3 grid(static_cast<unsigned>(p.N) * s.splits, s.tiles);
         norm_bwd_sums_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, dy, p.lddy,
-                                                                 p.ws, p.L, p.C, Cg, s.lanes, s.split_rows, p.act);
+                                                                 p.ws, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows, p.act);
         norm_bwd_join_kernel<<<static_cast<unsigned>(static_cast<long>(p.N) * p.G), kThreads, 0, st>>>(
             p.ws, p.weight, mom, p.L, p.G, Cg, s.splits);
         norm_bwd_apply_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, mom, dy,
-                                                                  p.lddy, dx, p.lddx, p.L, p.C, Cg, s.lanes,
-                                                                  s.split_rows, p.act);
+                                                                  p.lddy, dx, p.lddx, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows, p.act);
     }
     if (p.dw || p.db)
         norm_sum_kernel<<<static_cast<unsigned>((2L * p.C + 31) / 32), 1024, 0, st>>>(p.ws, p.dw, p.db, nblk,

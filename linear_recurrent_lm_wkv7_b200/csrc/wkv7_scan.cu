@@ -479,10 +479,12 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// The two kernels: this file's on warp-level products, two blocks per SM, and
-// wkv7_scan_tc.cu's.  Chunk times measured at B4 T1024 H32 N128 and B1 T16384 H40 N128.
+// The kernels: this file's on warp-level products, two blocks per SM in bf16 and one in
+// fp32, and wkv7_scan_tc.cu's.  (At B1 T16384 H40 N128 a chunk of 128 tokens takes the
+// latter 3.8 us with its outputs and 1.8 without.)
 constexpr CutCost kCutWarp{kChunk, 296, 0.5, 1.0, 2.0};
-constexpr CutCost kCutTc{128, 148, 0.45, 1.5, 4.0};
+constexpr CutCost kCutWarpF32{kChunk, 148, 0.5, 1.0, 1.0};
+constexpr CutCost kCutTc{128, 148, 0.5, 1.5, 2.0};
 // bf16 with N = 128 runs on the tcgen05 kernel (its tiles are 128 columns wide; rows are
 // numbered in 31 bits there).
 bool uses_tc(int io_dtype, int N, long rows) { return io_dtype == WKV7_BF16 && N == 128 && rows < (1L << 31); }
@@ -557,7 +559,8 @@ static size_t decays_bytes(int B, int T, int H, bool packed) {
     return static_cast<size_t>(chunk_slots(B, T, packed)) * H * sizeof(Decays);
 }
 size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
-    const size_t w = cut_floats(B, T, H, N, packed, kCutWarp) * sizeof(float) + decays_bytes(B, T, H, packed);
+    const size_t b = cut_floats(B, T, H, N, packed, kCutWarp), f = cut_floats(B, T, H, N, packed, kCutWarpF32);
+    const size_t w = (b > f ? b : f) * sizeof(float) + decays_bytes(B, T, H, packed);
     const size_t t = N == 128 ? cut_floats(B, T, H, N, packed, kCutTc) * sizeof(float) : 0;
     return w > t ? w : t;
 }
@@ -565,7 +568,7 @@ size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
 cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
     const bool packed = p.seq_offsets != nullptr;
     const bool tc = uses_tc(io_dtype, p.N, packed ? p.T : static_cast<long>(p.B) * p.T);
-    const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, packed, tc ? kCutTc : kCutWarp);
+    const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, packed, tc ? kCutTc : io_dtype == WKV7_BF16 ? kCutWarp : kCutWarpF32);
     const bool whole = map.seg >= p.T;
     uint8_t* ws = static_cast<uint8_t*>(p.ws);
     Decays* dec = reinterpret_cast<Decays*>(ws);

@@ -901,7 +901,7 @@ struct Plan {
 Plan plan_of(int B, int T, int H, int N, int G, int io_dtype, const int32_t* offs, bool packed) {
     Plan p;
     // both directions run at once; without segments the one pass makes states anyway
-    p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, 296, 1.0, 1.0, 2.0});
+    p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, io_dtype == WKV7_BF16 ? 296 : 148, 1.0, 1.0, 2.0});
     p.whole = p.seg.seg >= T;
     p.chunk = chunk_map(B, T, offs);
     p.seg_count = packed ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;

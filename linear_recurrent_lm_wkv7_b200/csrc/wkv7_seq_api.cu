@@ -73,23 +73,23 @@ int conv_check(int64_t B, int64_t T, int64_t C, int W, int act, int io_dtype, bo
 }
 
 // sizes shared by the scan's calls
-int scan_check(int64_t B, int64_t T, int64_t H, int D, int N, int G, int io_dtype, int dt_dtype) {
+int scan_check(int64_t B, int64_t T, int64_t H, int D, int N, int G, int io_dtype, int dt_dtype, bool packed) {
     if (B <= 0 || T < 0 || H <= 0 || D <= 0 || N <= 0 || G <= 0 || H % G != 0) return WKV7_ERR_INVALID_ARG;
     if (!dtype_ok(io_dtype) || !dtype_ok(dt_dtype)) return WKV7_ERR_INVALID_ARG;
     if (D != kHead || (N != 16 && N != 32 && N != 64 && N != 128)) return WKV7_ERR_UNSUPPORTED;
     // blocks, one or more per (sequence, head) or per (chunk, head), are numbered in 31 bits
-    if (H > kMaxChannels || (B * ((T + 63) / 64 + 1) + B) >= (int64_t(1) << 31) / H) return WKV7_ERR_UNSUPPORTED;
+    const int64_t slots = (packed ? T / 64 : B * ((T + 63) / 64)) + B;
+    if (H > kMaxChannels || slots >= (int64_t(1) << 31) / H) return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
 }
 
 int norm_check(int64_t N, int64_t L, int64_t C, int64_t G, int act, int io_dtype) {
     if (N < 0 || L < 0 || C <= 0 || G <= 0 || C % G != 0) return WKV7_ERR_INVALID_ARG;
     if (!dtype_ok(io_dtype) || !act_ok(act)) return WKV7_ERR_INVALID_ARG;
-    if (C > kMaxChannels || N * G >= (int64_t(1) << 31)) return WKV7_ERR_UNSUPPORTED;
+    // blocks, one per (sample, group) or a few per sample, are numbered in 31 bits
+    if (C > kMaxChannels || N * G >= (int64_t(1) << 31) || N >= (int64_t(1) << 30)) return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
 }
-// The split form of the group norm (see wkv7_norm.cu) numbers samples in a grid dimension.
-bool norm_too_many(int N, int L, int C, int G) { return N > 65535 && (L > 1 || C / G > 1024); }
 
 }  // namespace
 
@@ -173,7 +173,7 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
 }
 
 size_t wkv7_selective_scan_workspace_bytes(int B, int T, int H, int D, int N, int packed) {
-    if (scan_check(B, T, H, D, N, 1, WKV7_F32, WKV7_F32) != WKV7_OK) return 0;
+    if (scan_check(B, T, H, D, N, 1, WKV7_F32, WKV7_F32, packed != 0) != WKV7_OK) return 0;
     return T > 0 ? wkv7::scan_workspace_bytes(B, T, H, N, packed != 0) : 0;
 }
 
@@ -182,7 +182,7 @@ int wkv7_selective_scan(const void* x, int64_t ld_x, const void* dt, int64_t ld_
                         const float* s0, void* y, int64_t ld_y, float* sT, void* workspace, size_t workspace_bytes,
                         int B, int T, int H, int D, int N, int G, const int32_t* seq_offsets, int dt_softplus,
                         int io_dtype, int dt_dtype, void* stream) {
-    int s = scan_check(B, T, H, D, N, G, io_dtype, dt_dtype);
+    int s = scan_check(B, T, H, D, N, G, io_dtype, dt_dtype, seq_offsets != nullptr);
     if (s != WKV7_OK) return s;
     if (!A || (T > 0 && (!x || !dt || !Bm || !Cm || !y))) return WKV7_ERR_INVALID_ARG;
     const int64_t wx = static_cast<int64_t>(H) * D, wb = static_cast<int64_t>(G) * N;
@@ -217,7 +217,7 @@ int wkv7_selective_scan_step(const void* x, int64_t ld_x, const void* dt, int64_
                              const void* Bm, int64_t ld_b, const void* Cm, int64_t ld_c, const float* D_skip,
                              const float* dt_bias, const float* s_in, void* y, int64_t ld_y, float* s_out, int B,
                              int H, int D, int N, int G, int dt_softplus, int io_dtype, int dt_dtype, void* stream) {
-    int s = scan_check(B, 1, H, D, N, G, io_dtype, dt_dtype);
+    int s = scan_check(B, 1, H, D, N, G, io_dtype, dt_dtype, false);
     if (s != WKV7_OK) return s;
     if (!x || !dt || !A || !Bm || !Cm || !y || !s_out) return WKV7_ERR_INVALID_ARG;
     const int64_t wx = static_cast<int64_t>(H) * D, wb = static_cast<int64_t>(G) * N;
@@ -242,7 +242,7 @@ int wkv7_selective_scan_step(const void* x, int64_t ld_x, const void* dt, int64_
 
 size_t wkv7_selective_scan_backward_workspace_bytes(int B, int T, int H, int D, int N, int G, int io_dtype,
                                                     int packed) {
-    if (scan_check(B, T, H, D, N, G, io_dtype, WKV7_F32) != WKV7_OK) return 0;
+    if (scan_check(B, T, H, D, N, G, io_dtype, WKV7_F32, packed != 0) != WKV7_OK) return 0;
     return T > 0 ? wkv7::scan_backward_workspace_bytes(B, T, H, N, G, io_dtype, packed != 0) : 0;
 }
 
@@ -254,7 +254,7 @@ int wkv7_selective_scan_backward(const void* x, int64_t ld_x, const void* dt, in
                                  float* ds0, void* workspace, size_t workspace_bytes, int B, int T, int H, int D,
                                  int N, int G, const int32_t* seq_offsets, int dt_softplus, int io_dtype,
                                  int dt_dtype, void* stream) {
-    int s = scan_check(B, T, H, D, N, G, io_dtype, dt_dtype);
+    int s = scan_check(B, T, H, D, N, G, io_dtype, dt_dtype, seq_offsets != nullptr);
     if (s != WKV7_OK) return s;
     if (!A || !dA || (T > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dB || !dC || !workspace)))
         return WKV7_ERR_INVALID_ARG;
@@ -312,7 +312,6 @@ int wkv7_group_norm(const void* x, int64_t ld_x, const float* weight, const floa
     if (!(eps >= 0.f)) return WKV7_ERR_INVALID_ARG;
     const int64_t rows = static_cast<int64_t>(N) * L;
     if (rows > 0 && (!x || !y)) return WKV7_ERR_INVALID_ARG;
-    if (norm_too_many(N, L, C, G)) return WKV7_ERR_UNSUPPORTED;
     if (!ld_ok(ld_x, C) || !ld_ok(ld_y, C)) return WKV7_ERR_INVALID_ARG;
     if (misaligned({x, weight, bias, y, stats, workspace})) return WKV7_ERR_MISALIGNED;
     const size_t need = wkv7_group_norm_workspace_bytes(N, L, C, G, io_dtype);
@@ -342,7 +341,6 @@ int wkv7_group_norm_backward(const void* x, int64_t ld_x, const float* weight, c
     if (s != WKV7_OK) return s;
     const int64_t rows = static_cast<int64_t>(N) * L;
     if (rows > 0 && (!x || !stats || !dy || !dx)) return WKV7_ERR_INVALID_ARG;
-    if (norm_too_many(N, L, C, G)) return WKV7_ERR_UNSUPPORTED;
     if (!ld_ok(ld_x, C) || !ld_ok(ld_dy, C) || !ld_ok(ld_dx, C)) return WKV7_ERR_INVALID_ARG;
     if (misaligned({x, weight, bias, stats, dy, dx, dweight, dbias, workspace})) return WKV7_ERR_MISALIGNED;
     const size_t need = wkv7_group_norm_backward_workspace_bytes(N, L, C, G, io_dtype);

@@ -211,6 +211,75 @@ def test_scan_segments(wk, io):
         check_scan(wk, inp, offs)
 
 
+@pytest.mark.parametrize("T", [1, 127, 128, 129, 257, 400])
+@pytest.mark.parametrize("H,G", [(3, 1), (4, 2)])
+def test_scan_around_long_chunks(wk, T, H, G):
+    """bf16 with 128 state columns works in chunks of 128 tokens."""
+    check_scan(wk, scan_inputs((2, T), 2, H, 128, G, "bf16", seed=T + H))
+
+
+def test_scan_long_chunks_segments(wk):
+    lens = [1700, 0, 1, 1300]
+    for lead, B, offs in (((1, 3000), 1, None), ((sum(lens),), 4, offsets(lens))):
+        check_scan(wk, scan_inputs(lead, B, 2, 128, 1, "bf16", seed=12, decay=(0.01, 0.1)), offs)
+
+
+@pytest.mark.parametrize("io,N", [("f32", 32), ("bf16", 32), ("bf16", 128)])
+def test_scan_keeps_sequences_apart(wk, io, N):
+    """Infinities and NaN in one packed sequence leave the others' bits alone."""
+    lens = [70, 60, 130, 5]
+    inp = scan_inputs((sum(lens),), 4, 4, N, 2, io, seed=N)
+    d = {k: cuda(v) for k, v in inp.items()}
+    offs = offsets(lens)
+    bad = slice(int(offs[1]), int(offs[2]))
+    ill = {k: v.clone() for k, v in d.items()}
+    for k in ("x", "Bm", "Cm", "dt", "dy"):
+        ill[k][bad] = float("nan")
+        ill[k][bad.start] = float("inf")
+    ill["s0"][1] = float("nan")
+    outs = []
+    for v in (d, ill):
+        kw = dict(D=v["D"], dt_bias=v["dt_bias"], s0=v["s0"], seq_offsets=offs.cuda())
+        y, sT = wk.selective_scan(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], **kw)
+        g = wk.selective_scan_backward(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], v["dy"], dsT=v["dsT"], **kw)
+        outs.append((y, sT, g[0], g[1], g[3], g[4], g[7]))
+    assert wk.wkv7_get_device_status() == 0
+    rows = torch.ones(sum(lens), dtype=torch.bool)
+    rows[bad] = False
+    seqs = torch.tensor([True, False, True, True])
+    for i, (a, b) in enumerate(zip(*outs)):
+        keep = (seqs if i in (1, 6) else rows).cuda()
+        assert torch.equal(a[keep], b[keep]), i
+
+
+def test_scan_many_sequences(wk):
+    """Hundreds of packed sequences of a few tokens, and their states."""
+    g = torch.Generator().manual_seed(0)
+    lens = torch.randint(0, 4, (300,), generator=g).tolist()
+    for io, N in (("f32", 16), ("bf16", 128)):
+        inp = scan_inputs((sum(lens),), 300, 2, N, 1, io, seed=1)
+        check_scan(wk, inp, offsets(lens), longest=3)
+
+
+def test_calls_on_two_streams(wk):
+    """The same kernels from two streams at once."""
+    ins = []
+    for seed in (1, 2):
+        inp = scan_inputs((1, 3000), 1, 4, 128, 1, "bf16", seed=seed)
+        ins.append({k: cuda(v) for k, v in inp.items()})
+    call = lambda d, st=None: wk.selective_scan(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], D=d["D"], dt_bias=d["dt_bias"],
+                                                s0=d["s0"], stream=st)
+    want = [call(d) for d in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [[call(d, st) for _ in range(5)] for d, st in zip(ins, streams)]
+    torch.cuda.synchronize()
+    assert wk.wkv7_get_device_status() == 0
+    for w, gs in zip(want, got):
+        for y, sT in gs:
+            assert torch.equal(y, w[0]) and torch.equal(sT, w[1])
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_scan_without_options(wk, io):
     """No skip, bias, state or softplus; delta given as it is, zeros among it."""
@@ -381,6 +450,45 @@ def test_norm_over_tokens(wk, io, N, L, C, groups):
 def test_norm_far_from_zero(wk, shape):
     """A mean of a thousand deviations: the squares are taken about the mean."""
     check_norm(wk, shape, 2, "f32", None, shift=1000.0)
+
+
+def test_norm_many_samples(wk):
+    """More samples than a grid dimension but the first holds."""
+    x = torch.randn(70000, 2, 12, generator=torch.Generator().manual_seed(3))
+    ref = R.norm(x, 3, activation="silu", dy=x)
+    y, stats = wk.group_norm(x.cuda(), 3, act="silu", want_stats=True)
+    dx, _, _ = wk.group_norm_backward(x.cuda(), 3, stats, x.cuda(), act="silu")
+    assert float((y.cpu().double() - ref["y"]).norm() / ref["y"].norm()) < 2.0 ** -20
+    assert float((dx.cpu().double() - ref["dx"]).norm() / ref["dx"].norm()) < 2.0 ** -18
+
+
+def test_norm_keeps_samples_apart(wk):
+    for shape in ((6, 64), (6, 40, 64)):
+        x = torch.randn(shape, generator=torch.Generator().manual_seed(4)).cuda()
+        y = wk.group_norm(x, 4, act="silu")
+        ill = x.clone()
+        ill[2] = float("nan")
+        ill[4] = float("inf")
+        z = wk.group_norm(ill, 4, act="silu")
+        keep = [0, 1, 3, 5]
+        assert torch.equal(y[keep], z[keep])
+
+
+def test_conv_keeps_sequences_apart(wk):
+    inp = conv_inputs((60,), 3, 24, 4, "bf16", seed=6)
+    offs = offsets([20, 21, 19]).cuda()
+    d = {k: cuda(v) for k, v in inp.items()}
+    ill = {k: v.clone() for k, v in d.items()}
+    ill["x"][20:41] = float("nan")
+    ill["s0"][1] = float("inf")
+    outs = [(*wk.causal_conv(v["x"], v["w"], v["bias"], v["s0"], offs, "silu"),
+             *wk.causal_conv_backward(v["x"], v["w"], v["dy"], v["bias"], v["s0"], v["dsT"], offs, "silu")[::3])
+            for v in (d, ill)]
+    keep = torch.ones(60, dtype=torch.bool)
+    keep[20:41] = False
+    for i, (a, b) in enumerate(zip(*outs)):
+        k = torch.tensor([True, False, True]).cuda() if i in (1, 3) else keep.cuda()
+        assert torch.equal(a[k], b[k]), i
 
 
 def test_norm_constant_rows(wk):

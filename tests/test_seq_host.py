@@ -106,7 +106,7 @@ def test_scan_refusals(wk, step):
     if step:
         assert call(sT=None) == -1
     else:
-        assert call(T=-1) == -1 and call(T=(1 << 31) - 1, H=1 << 12) == -2
+        assert call(T=-1) == -1 and call(T=(1 << 31) - 1, H=1 << 12, ldx=1 << 18, ldy=1 << 18, lddt=1 << 12) == -2
         # a case that works in segments needs its workspace
         need = wk.wkv7_selective_scan_workspace_bytes(1, 20000, 4, 64, 32, False)
         assert need > 0 and call(B=1, T=20000, ws=None) == -1 and call(B=1, T=20000, wsb=need - 1) == -1
@@ -145,7 +145,7 @@ def test_norm_refusals(wk):
     assert call(eps=-1.0) == -1 and call(eps=float("nan")) == -1 and call(act=9) == -1 and call(io=2) == -1
     assert call(x=None) == -1 and call(y=None) == -1 and call(y=ok["x"]) == -1 and call(ldx=60) == -1
     assert call(x=ok["x"] + 2) == -3 and call(stats=ok["y"] + 16) == -1
-    assert call(N=1 << 20, L=2) == -2
+    assert call(N=1 << 30) == -2 and call(N=1 << 29, C=64, G=4) == -2
     need = wk.wkv7_group_norm_workspace_bytes(3, 50, 64, 4, 1)
     assert need > 0 and call(L=50, ws=None) == -1 and call(L=50, wsb=need - 1) == -1
     assert wk.wkv7_group_norm_workspace_bytes(3, 1, 64, 4, 1) == 0
