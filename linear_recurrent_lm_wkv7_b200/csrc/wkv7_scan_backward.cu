@@ -18,36 +18,14 @@
 //
 // Launches: the decays; (1) the states S_0 and the gradients dS at every chunk boundary, forwards
 // and backwards side by side, written as bf16 planes (over segments where sequences
-// and heads are few, as in wkv7_scan.cu); (2) one block per chunk, group and share of
+// and heads are few, as in wkv7_scan.cu; on tcgen05 in wkv7_scan_tc.cu for bf16 and N = 128); (2) one block per chunk, group and share of
 // the group's heads, which keeps the sums over heads in registers: warps 0-3 hold 16
 // tokens t each (dC, E, sums over s), warps 4-7 16 tokens s each (dx, dB, F, sums over
 // t); (3) sums over the shares and over chunks, in a fixed order.
-#include "scan_common.cuh"
+#include "scan_backward.cuh"
 
 namespace wkv7 {
 namespace {
-
-struct BwdDev {
-    const void *x, *Bm, *Cm, *dy;
-    long ldx, ldb, ldc, lddy;
-    const float *A, *D, *s0, *dsT;
-    void *dx, *ddt, *dB, *dC;
-    long lddx, ldddt, lddb, lddc;
-    float *dA, *dD, *dbias, *ds0;
-    int H, G, softplus, dt_bf16;
-    SegMap seg, chunk;   // segments, and the same cut at 64 tokens
-    long seg_count, chunk_count;
-    // workspace
-    const Decays* dec;      // [chunk][H]
-    __nv_bfloat16* states;  // [2][chunk][H][plane][64][N]: S_0 and dS
-    float* seg_state;       // [2][seg][H][64][N]
-    float* seg_decay;       // [seg][H]
-    float* part;            // [2][share][row][G N]: dB and dC of a share of the heads
-    float* scalars;         // [chunk][H][4]: dA, d dt_bias, dD
-    int shares;
-    long rows;
-    int* status;
-};
 
 // ---------------------------------------------------------------- (1) states
 template <typename IO, int N>
@@ -276,7 +254,9 @@ struct GradLayout {
     static constexpr int PI = kInPlanes<IO>, PC = kCalcPlanes<IO>;
     using TX = Tile<PI, kChunk, kScanP>;
     using TB = Tile<PI, kChunk, N>;
-    using TS = Tile<kStatePlanes, kScanP, N>;
+    static constexpr bool transposed = kStatesT<IO, N>;
+    static constexpr int s_rows = transposed ? N : kScanP, s_cols = transposed ? kScanP : N;
+    using TS = Tile<kStatePlanes, s_rows, s_cols>;
     // bf16: the next head's rows of x and dy are copied while this one is worked on, its
     // states once this one's have been used.  fp32: one stage, in which S_0 and dS take
     // turns in one place.
@@ -383,10 +363,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
     auto stage = [&](int i) { return (i % LY::stages) * LY::stage_bytes; };
     auto load_state = [&](int off, int back, int h) {
         const __nv_bfloat16* src = a.states + (((back ? a.chunk_count : 0) + slot) * a.H + h) * (kStatePlanes * kState);
-        constexpr int per = N / 8;
-        for (int i = tid; i < kStatePlanes * kScanP * per; i += kScanThreads) {
+        constexpr int per = LY::s_cols / 8;
+        for (int i = tid; i < kStatePlanes * LY::s_rows * per; i += kScanThreads) {
             const int r = i / per, c = i % per;
-            cp_async16(sb + off + r * TS::pitch + c * 16, src + r * N + c * 8, true);  // planes follow each other
+            const int to = LY::transposed ? c ^ (r & 7) : c;  // planes follow each other
+            cp_async16(sb + off + r * TS::pitch + to * 16, src + i * 8, true);
         }
     };
     auto load = [&](int i) {
@@ -519,7 +500,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
 #pragma unroll
                     for (int j = 0; j < NB / 8; j += 2) {
                         uint32_t fb[2][kStatePlanes][2];
-                        frag_b_t<TS>(fb, sb + ostate, nb + j * 8, k, lane);
+                        if constexpr (LY::transposed)
+                            frag_b<TS>(fb, sb + ostate, nb + j * 8, k, lane);
+                        else
+                            frag_b_t<TS>(fb, sb + ostate, nb + j * 8, k, lane);
                         mma_planes<PI, kStatePlanes>(v[j], fa, fb[0]);
                         mma_planes<PI, kStatePlanes>(v[j + 1], fa, fb[1]);
                     }
@@ -563,13 +547,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             for (int k = 0; k < kState / 8 / kScanThreads + (kState / 8 % kScanThreads ? 1 : 0); ++k) {
                 const int p = tid + k * kScanThreads;
                 if (kState / 8 % kScanThreads && p >= kState / 8) continue;
-                const int r = p / (N / 8), c = p % (N / 8) * 8;  // eight columns of a row
+                const int r = p / (LY::s_cols / 8), c = p % (LY::s_cols / 8) * 8;  // eight columns of a row
                 uint4 u[kStatePlanes], v[kStatePlanes];
 #pragma unroll
                 for (int w = 0; w < kStatePlanes; ++w) {
                     u[w] = *reinterpret_cast<const uint4*>(smem + ods + w * TS::plane + r * TS::pitch + c * 2);
                     if constexpr (LY::shared_state)
-                        v[w] = *reinterpret_cast<const uint4*>(g + w * kState + r * N + c);
+                        v[w] = *reinterpret_cast<const uint4*>(g + w * kState + r * LY::s_cols + c);
                     else
                         v[w] = *reinterpret_cast<const uint4*>(smem + os0 + w * TS::plane + r * TS::pitch + c * 2);
                 }
@@ -600,7 +584,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     uint32_t fb[2][kStatePlanes][2];
-                    frag_b<TS>(fb, sb + ods, j * 8, k, lane);
+                    if constexpr (LY::transposed)
+                        frag_b_t<TS>(fb, sb + ods, j * 8, k, lane);
+                    else
+                        frag_b<TS>(fb, sb + ods, j * 8, k, lane);
                     mma_planes<PI, kStatePlanes>(X[j], fa, fb[0]);
                     mma_planes<PI, kStatePlanes>(X[j + 1], fa, fb[1]);
                 }
@@ -901,7 +888,8 @@ struct Plan {
 Plan plan_of(int B, int T, int H, int N, int G, int io_dtype, const int32_t* offs, bool packed) {
     Plan p;
     // both directions run at once; without segments the one pass makes states anyway
-    p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, io_dtype == WKV7_BF16 ? 296 : 148, 1.0, 1.0, 2.0});
+    const int resident = io_dtype == WKV7_BF16 && N != 128 ? 296 : 148;
+    p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, resident, 1.0, 1.0, 2.0});
     p.whole = p.seg.seg >= T;
     p.chunk = chunk_map(B, T, offs);
     p.seg_count = packed ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;
@@ -925,18 +913,32 @@ cudaError_t bwd_typed(const BwdDev& d, const Plan& p, cudaStream_t st) {
     using SL = StateLayout<IO, N>;
     using GL = GradLayout<IO, N>;
     static std::atomic<unsigned long long> cfg_w{0}, cfg_s{0}, cfg_g{0};
-    cudaError_t e = configure_smem_once(scan_states_kernel<IO, N, true>, SL::bytes, cfg_w);
-    if (e == cudaSuccess) e = configure_smem_once(scan_grad_kernel<IO, N>, GL::bytes, cfg_g);
-    if (e == cudaSuccess && !p.whole) e = configure_smem_once(scan_states_kernel<IO, N, false>, SL::bytes, cfg_s);
+    cudaError_t e = configure_smem_once(scan_grad_kernel<IO, N>, GL::bytes, cfg_g);
+    if constexpr (!kStatesT<IO, N>) {
+        if (e == cudaSuccess) e = configure_smem_once(scan_states_kernel<IO, N, true>, SL::bytes, cfg_w);
+        if (e == cudaSuccess && !p.whole) e = configure_smem_once(scan_states_kernel<IO, N, false>, SL::bytes, cfg_s);
+    }
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(p.seg_count * d.H), 2);
+    constexpr bool tc = kStatesT<IO, N>;
+    auto states = [&](bool write) {
+        if constexpr (tc) {
+            e = launch_states_tc(d, write, write && p.whole, st);
+        } else if (write) {
+            scan_states_kernel<IO, N, true><<<grid, kScanThreads, SL::bytes, st>>>(d, p.whole);
+        } else {
+            scan_states_kernel<IO, N, false><<<grid, kScanThreads, SL::bytes, st>>>(d, false);
+        }
+    };
     if (!p.whole) {
-        scan_states_kernel<IO, N, false><<<grid, kScanThreads, SL::bytes, st>>>(d, false);
+        states(false);
+        if (e != cudaSuccess) return e;
         constexpr int elems = kScanP * N;
         scan_states_join_kernel<<<dim3(static_cast<unsigned>(p.seg.B) * d.H, (elems / 4 + 255) / 256, 2), 256, 0,
                                   st>>>(d, elems);
     }
-    scan_states_kernel<IO, N, true><<<grid, kScanThreads, SL::bytes, st>>>(d, p.whole);
+    states(true);
+    if (e != cudaSuccess) return e;
     scan_grad_kernel<IO, N>
         <<<static_cast<unsigned>(p.chunk_count * d.G * d.shares), kScanThreads, GL::bytes, st>>>(d);
     const int width = d.G * N;

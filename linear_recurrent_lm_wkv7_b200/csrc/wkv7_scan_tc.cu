@@ -27,7 +27,7 @@
 // touch no tensor memory are therefore put on the first quarters.
 #include <cuda.h>
 
-#include "scan_common.cuh"
+#include "scan_backward.cuh"
 #include "tma_host.cuh"
 
 namespace wkv7 {
@@ -537,10 +537,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             issued = c + 1;
         }
-        // nothing may still be on its way into shared memory when the block ends
-        if (!ok)
-            for (int c = issued < kStages ? 0 : issued - kStages; c < issued; ++c)
-                mbar_wait(&bar.full[c % kStages], static_cast<uint32_t>(c / kStages) & 1u, 2000000000ull);
+        // nothing may still be on its way into shared memory when the block ends, also
+        // where other warps gave up
+        for (int c = issued < kStages ? 0 : issued - kStages; c < issued; ++c)
+            mbar_wait(&bar.full[c % kStages], static_cast<uint32_t>(c / kStages) & 1u, 2000000000ull);
     } else if (warp >= kWarpDec) {
         // ------------------------------------------------------------ decays
         const float Ah = a.A[h], bias = a.bias ? a.bias[h] : 0.f;
@@ -681,13 +681,294 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-// rows x width matrix of bf16 at a row stride, box 64 columns x 128 rows
-bool make_map(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint64_t ld) {
+// ---------------------------------------------------------------- states of the backward
+// As scan_states_kernel (wkv7_scan_backward.cu): blockIdx.y 0 walks the states forwards from
+// x and B, 1 their gradients backwards from dy and C, in chunks of 64 tokens, and with
+// WRITE leaves each at every chunk.  Product (4) alone, K = 64, with the chunks' decays
+// loaded like the rows.  18 warps: 0-7 the state (lane n, half of p each), 8-15 the scaled
+// rows in two groups that take pieces of 32 tokens in turn, 16 loads, 17 products, 18 stores.
+// A state leaves as one bulk copy of its 48 KB out of two buffers.  At B4 T1024 H32 (201 MB
+// written) 49.7 us, 4.0 TB/s, 12 % of it an uneven second wave of blocks; 59.9 us with one
+// buffer, 93 us stored from the registers, 74 us in scan_states_kernel's form on mma.sync.
+constexpr int kStStages = 3, kStRing = 4, kStOuts = 2, kStThreads = 19 * 32;
+constexpr uint32_t kStTile = kChunk * 128;  // 64 rows of 128 bytes
+constexpr uint32_t kStStage = 3 * kStTile;
+constexpr uint32_t kStOffXw = kStStages * kStStage;
+constexpr uint32_t kStOffOut = kStOffXw + kStRing * 3 * kPiece;
+constexpr uint32_t kStOut = 3 * kScanP * kN * 2;  // a state in planes
+constexpr uint32_t kStOffDec = kStOffOut + kStOuts * kStOut;
+constexpr uint32_t kStOffBar = kStOffDec + kStStages * static_cast<uint32_t>(sizeof(Decays));
+struct StBars {
+    uint64_t full[kStStages], empty[kStStages], xw_full[kStRing], xw_empty[kStRing], d_full[2], d_empty[2], out_full[kStOuts], out_empty[kStOuts], fin;
+    uint32_t tmem;
+};
+constexpr uint32_t kStSmem = kStOffBar + sizeof(StBars) + 1024;
+static_assert(kStOffBar % 8 == 0 && kStSmem <= 227 * 1024, "shared memory of an SM");
+
+struct StMaps {
+    CUtensorMap x, b, dy, c;
+};
+
+template <bool WRITE>
+__global__ void __launch_bounds__(kStThreads, 1)
+    states_tc_kernel(const BwdDev a, bool whole, const __grid_constant__ StMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    StBars& bar = *reinterpret_cast<StBars*>(sm + kStOffBar);
+    const Decays* dec = reinterpret_cast<const Decays*>(sm + kStOffDec);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int back = blockIdx.y, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
+    const long slot = blockIdx.x / a.H;
+    constexpr long kState = static_cast<long>(kScanP) * kN;
+
+    int n;
+    long r0, r1, lo, hi;
+    if (!seg_rows(a.seg, slot, n, r0, r1, lo, hi, a.status)) {
+        if (!whole || !back || !a.ds0 || hi > lo || slot != seg_first(a.seg, n, lo)) return;
+        const long e = (static_cast<long>(n) * a.H + h) * kState;  // no tokens: ds0 = dsT
+        for (int i = tid; i < kState; i += kStThreads) a.ds0[e + i] = a.dsT ? a.dsT[e + i] : 0.f;
+        return;
+    }
+    const long seq_state = (static_cast<long>(n) * a.H + h) * kState;
+    float* slot_state = a.seg_state + ((back ? a.seg_count : 0) + slot) * a.H * kState + h * kState;
+    const int rows = static_cast<int>(r1 - r0), chunks = (rows + kChunk - 1) / kChunk;
+    const long chunk0 = seg_first(a.chunk, n, lo) + (r0 - lo) / kChunk;
+    auto at_chunk = [&](int i) { return back ? chunks - 1 - i : i; };  // the i-th of the walk
+
+    if (warp == 17) {
+        if (lane == 0) {
+            for (int i = 0; i < kStStages; ++i) {
+                mbar_init(&bar.full[i], 1);
+                mbar_init(&bar.empty[i], 17);  // the products, and the warps that read decays and rows
+            }
+            for (int i = 0; i < kStRing; ++i) {
+                mbar_init(&bar.xw_full[i], 4);
+                mbar_init(&bar.xw_empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bar.d_full[i], 1);
+                mbar_init(&bar.d_empty[i], 8);
+            }
+            for (int i = 0; i < kStOuts; ++i) {
+                mbar_init(&bar.out_full[i], 8);
+                mbar_init(&bar.out_empty[i], 1);
+            }
+            mbar_init(&bar.fin, 1);
+            fence_mbar_init();
+        }
+        tmem_alloc(&bar.tmem, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = bar.tmem;
+    bool ok = true;
+    auto wait = [&](uint64_t& b, int k) {
+        for (uint32_t i = 0; ok && !__all_sync(0xffffffffu, mbar_try_wait_sleep(&b, k & 1, kPollNs)); ++i)
+            ok = i < kPolls;
+    };
+    auto signal = [&](uint64_t& b) {  // once per warp
+        __syncwarp();
+        if (lane == 0) arrive(&b);
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ the state
+        const int row = 32 * (warp & 3) + lane, p0 = warp >= 4 ? kHalf : 0;
+        const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
+        float S[kHalf];
+        {
+            const float* first = back ? a.dsT : a.s0;
+            const float* src = whole ? (first ? first + seq_state : nullptr) : WRITE ? slot_state : nullptr;
+#pragma unroll
+            for (int p = 0; p < kHalf; ++p) S[p] = src ? src[(p0 + p) * kN + row] : 0.f;
+        }
+        float run = 1.f;
+        for (int i = 0; i < chunks && ok; ++i) {
+            if constexpr (WRITE) {
+                const int o = i % kStOuts;
+                if (i >= kStOuts) wait(bar.out_empty[o], i / kStOuts - 1);
+                if (!ok) break;
+#pragma unroll
+                for (int p = 0; p < kHalf; p += 8) {
+                    uint32_t u[4][3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split_pair<3>(u[e], S[p + 2 * e], S[p + 2 * e + 1]);
+#pragma unroll
+                    for (int w = 0; w < 3; ++w)
+                        *reinterpret_cast<uint4*>(sm + kStOffOut + o * kStOut + w * (kState * 2) +
+                                                  swz(row, (p0 + p) * 2, kN)) =
+                            make_uint4(u[0][w], u[1][w], u[2][w], u[3][w]);
+                }
+                fence_proxy_async_smem();
+                signal(bar.out_full[o]);
+            }
+            wait(bar.full[i % kStStages], i / kStStages);
+            const float tot = dec[i % kStStages].total;
+            signal(bar.empty[i % kStStages]);
+            wait(bar.d_full[i & 1], i >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            run *= tot;
+            float v[2][16];
+            __syncwarp();
+            tmem_load16(tm + lane_base + 64 * (i & 1) + p0, v[0]);
+            tmem_load16(tm + lane_base + 64 * (i & 1) + p0 + 16, v[1]);
+            tmem_wait(v[0]);
+            tmem_wait(v[1]);
+            tc_fence_before();
+            signal(bar.d_empty[i & 1]);
+#pragma unroll
+            for (int e = 0; e < kHalf; e += 2) {
+                const float2 r = fma2(make_float2(tot, tot), make_float2(S[e], S[e + 1]),
+                                      make_float2(v[e / 16][e % 16], v[e / 16][e % 16 + 1]));
+                S[e] = r.x, S[e + 1] = r.y;
+            }
+        }
+        float* dst = !WRITE ? slot_state : whole && back && a.ds0 ? a.ds0 + seq_state : nullptr;
+        if (ok && dst) {
+#pragma unroll
+            for (int p = 0; p < kHalf; ++p) dst[(p0 + p) * kN + row] = S[p];
+        }
+        if (!WRITE && !back && warp == 0 && lane == 0) a.seg_decay[slot * a.H + h] = run;
+    } else if (warp < 16) {
+        // ------------------------------------------------------------ the scaled rows
+        const int group = (warp - 8) >> 2, w = (warp & 3) * 32 + lane, r = w >> 2, part = (w & 3) * 32;
+        for (int i = 0; i < chunks && ok; ++i) {  // piece `group` of every chunk
+            const int s = 32 * group + r, ring = (2 * i + group) % kStRing, left = rows - at_chunk(i) * kChunk;
+            const Decays& d = dec[i % kStStages];
+            uint8_t* st = sm + (i % kStStages) * kStStage;
+            wait(bar.full[i % kStStages], i / kStStages);
+            if (2 * i + group >= kStRing) wait(bar.xw_empty[ring], (2 * i + group) / kStRing - 1);
+            if (!ok) break;
+            const bool live = s < left;
+            const float f = back ? d.from[s] : d.delta[s] * d.to[s];
+            uint8_t* out = sm + kStOffXw + ring * 3 * kPiece;
+#pragma unroll
+            for (int b = 0; b < 32; b += 16) {
+                uint4 xv = *reinterpret_cast<const uint4*>(st + swz(s, part + b, kChunk));
+                if (!live) {  // rows of the next sequence, as in scan_tc_kernel
+                    xv = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(st + kStTile + swz(s, part + b, kChunk)) = xv;
+                    *reinterpret_cast<uint4*>(st + 2 * kStTile + swz(s, part + b, kChunk)) = xv;
+                }
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t u[4][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = mul2(make_float2(f, f), make_float2(bf_lo(xw[e]), bf_hi(xw[e])));
+                    split_pair<3>(u[e], v.x, v.y);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    *reinterpret_cast<uint4*>(out + p * kPiece + swz(r, part + b, 32)) =
+                        make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
+            }
+            fence_proxy_async_smem();
+            signal(bar.xw_full[ring]);
+            signal(bar.empty[i % kStStages]);
+        }
+    } else if (warp == 16) {
+        // ------------------------------------------------------------ loads
+        int issued = 0;
+        for (int i = 0; i < chunks && ok; ++i) {
+            const int st = i % kStStages;
+            if (i >= kStStages) wait(bar.empty[st], i / kStStages - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                uint8_t* p = sm + st * kStStage;
+                const int row = static_cast<int>(r0 + static_cast<long>(at_chunk(i)) * kChunk);
+                const CUtensorMap *mx = back ? &maps.dy : &maps.x, *mb = back ? &maps.c : &maps.b;
+                mbar_arrive_expect_tx(&bar.full[st], kStStage + static_cast<uint32_t>(sizeof(Decays)));
+                tma_load_2d(p, mx, &bar.full[st], h * kScanP, row);
+                tma_load_2d(p + kStTile, mb, &bar.full[st], grp * kN, row);
+                tma_load_2d(p + 2 * kStTile, mb, &bar.full[st], grp * kN + 64, row);
+                bulk_load(sm + kStOffDec + st * sizeof(Decays), a.dec + (chunk0 + at_chunk(i)) * a.H + h,
+                          sizeof(Decays), &bar.full[st]);
+            }
+            __syncwarp();
+            issued = i + 1;
+        }
+        // nothing may still be on its way into shared memory when the block ends
+        for (int i = issued < kStStages ? 0 : issued - kStStages; i < issued; ++i)
+            mbar_wait(&bar.full[i % kStStages], static_cast<uint32_t>(i / kStStages) & 1u, 2000000000ull);
+    } else if (warp == 18) {
+        // ------------------------------------------------------------ stores
+        if constexpr (WRITE) {
+            for (int i = 0; i < chunks && ok; ++i) {
+                const int o = i % kStOuts;
+                wait(bar.out_full[o], i / kStOuts);
+                if (!ok) break;
+                if (lane == 0) {
+                    bulk_store(a.states + (((back ? a.chunk_count : 0) + chunk0 + at_chunk(i)) * a.H + h) *
+                                              (kStatePlanes * kState),
+                               sm + kStOffOut + o * kStOut, kStOut);
+                    bulk_commit();
+                    bulk_wait_read<kStOuts - 1>();
+                    if (i >= kStOuts - 1) arrive(&bar.out_empty[(i + 1) % kStOuts]);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------ products
+        const uint64_t dB = desc_mn(sb + kStTile, kStTile), dXw = desc_mn(sb + kStOffXw, kPiece);
+        for (int i = 0; i < chunks && ok; ++i) {
+            const int st = i % kStStages;
+            wait(bar.full[st], i / kStStages);
+            if (i >= 2) wait(bar.d_empty[i & 1], (i >> 1) - 1);
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                const int piece = 2 * i + k, ring = piece % kStRing;
+                wait(bar.xw_full[ring], piece / kStRing);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t p = dB + st * at(kStStage) + step_mn(2 * k);
+                    uint64_t q = dXw + ring * at(3 * kPiece);
+#pragma unroll 1
+                    for (int w = 0; w < 3; ++w, q += at(kPiece)) {
+                        mma_smem(tm + 64 * (i & 1), p, q, kIdS, k > 0 || w > 0);
+                        mma_smem(tm + 64 * (i & 1), p + step_mn(1), q + step_mn(1), kIdS, true);
+                    }
+                    mma_commit(&bar.xw_empty[ring]);
+                    if (k == 1) {
+                        mma_commit(&bar.d_full[i & 1]);
+                        mma_commit(&bar.empty[st]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) mma_commit(&bar.fin);
+        __syncwarp();
+        const bool before = ok;
+        ok = true;
+        wait(bar.fin, 0);
+        ok = ok && before;
+    }
+    __syncwarp();
+    if (!ok && lane == 0) report_status(a.status, WKV7_ERR_DEVICE_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tm, 128);
+    }
+}
+
+// rows x width matrix of bf16 at a row stride, box 64 columns x `box_rows`
+bool make_map(CUtensorMap* m, const void* base, uint64_t width, uint64_t rows, uint64_t ld, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {width, rows};
     const cuuint64_t strides[1] = {ld * 2};
-    const cuuint32_t box[2] = {64, kL};
+    const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -700,9 +981,9 @@ cudaError_t launch_scan_tc(const ScanArgs& p, const SegMap& map, bool whole, boo
                            float* seg_decay, cudaStream_t stream) {
     TcMaps maps;
     const uint64_t rows = p.seq_offsets ? p.T : static_cast<uint64_t>(p.B) * p.T;
-    if (!make_map(&maps.x, p.x, static_cast<uint64_t>(p.H) * kScanP, rows, p.ldx) ||
-        !make_map(&maps.b, p.Bm, static_cast<uint64_t>(p.G) * kN, rows, p.ldb) ||
-        !make_map(&maps.c, p.Cm, static_cast<uint64_t>(p.G) * kN, rows, p.ldc))
+    if (!make_map(&maps.x, p.x, static_cast<uint64_t>(p.H) * kScanP, rows, p.ldx, kL) ||
+        !make_map(&maps.b, p.Bm, static_cast<uint64_t>(p.G) * kN, rows, p.ldb, kL) ||
+        !make_map(&maps.c, p.Cm, static_cast<uint64_t>(p.G) * kN, rows, p.ldc, kL))
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> cfg_out{0}, cfg_state{0};
     const TcArgs a{p.dt, p.lddt, p.ldy, p.A, p.D, p.dt_bias, p.s0, static_cast<__nv_bfloat16*>(p.y), p.sT, seg_state,
@@ -715,6 +996,26 @@ cudaError_t launch_scan_tc(const ScanArgs& p, const SegMap& map, bool whole, boo
     } else {
         e = configure_smem_once(scan_tc_kernel<false>, kTcSmem, cfg_state);
         if (e == cudaSuccess) scan_tc_kernel<false><<<grid, kTcThreads, kTcSmem, stream>>>(a, whole, maps);
+    }
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_states_tc(const BwdDev& d, bool write, bool whole, cudaStream_t stream) {
+    StMaps maps;
+    const uint64_t rows = static_cast<uint64_t>(d.rows), wx = static_cast<uint64_t>(d.H) * kScanP,
+                   wb = static_cast<uint64_t>(d.G) * kN;
+    if (!make_map(&maps.x, d.x, wx, rows, d.ldx, kChunk) || !make_map(&maps.dy, d.dy, wx, rows, d.lddy, kChunk) ||
+        !make_map(&maps.b, d.Bm, wb, rows, d.ldb, kChunk) || !make_map(&maps.c, d.Cm, wb, rows, d.ldc, kChunk))
+        return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> cfg_w{0}, cfg_s{0};
+    const dim3 grid(static_cast<unsigned>(d.seg_count * d.H), 2);
+    cudaError_t e;
+    if (write) {
+        e = configure_smem_once(states_tc_kernel<true>, kStSmem, cfg_w);
+        if (e == cudaSuccess) states_tc_kernel<true><<<grid, kStThreads, kStSmem, stream>>>(d, whole, maps);
+    } else {
+        e = configure_smem_once(states_tc_kernel<false>, kStSmem, cfg_s);
+        if (e == cudaSuccess) states_tc_kernel<false><<<grid, kStThreads, kStSmem, stream>>>(d, whole, maps);
     }
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
