@@ -393,8 +393,9 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
  * D must be 64, N one of 16, 32, 64 and 128, G a divisor of H.  x, Bm, Cm and y need
  * row strides of a multiple of 16 bytes; dt only the alignment of its elements.
  * A dt of -inf leaves the state as it is (padding): x, Bm and Cm of such a token must
- * still be finite.  Prompts are worked on in chunks of 64 tokens, so an infinity or
- * NaN in x, Bm or Cm may reach the outputs of earlier tokens of its chunk.
+ * still be finite.  Prompts are worked on in chunks of 64 tokens (128 for bf16
+ * with N = 128), so an infinity or NaN in x, Bm or Cm may reach the outputs of earlier
+ * tokens of its chunk.  Rows are numbered in 31 bits: B T >= 2^31 is refused.
  * wkv7_selective_scan_step: one token per sequence, B rows; s_out may be s_in (NULL:
  * zeros).
  * wkv7_selective_scan_backward: the gradient of <dy, y> + <dsT, sT>.

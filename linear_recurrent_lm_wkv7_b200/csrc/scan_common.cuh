@@ -180,7 +180,8 @@ __device__ __forceinline__ void chunk_decays(Decays& d, float dt0, float dt1, in
 // The decays of every (chunk slot, head) of `map` (segments of one chunk): out [slot][H].
 // Made once, by a warp each: a chunk's take thousands of cycles of dependent steps
 // (softplus, a scan in 64 bits), which in the kernels that walk chunks one after the
-// other would stand in the way of every chunk@@MEAS@@.
+// other would stand in the way of every chunk (with each kernel making its own, states of
+// the backward 117 us against 108 and gradients 170 against 165 at B4 T1024 H32 N128).
 struct DecayArgs {
     const void* dt;
     long lddt;

@@ -15,6 +15,11 @@
 // segments: a first pass takes every segment's state from zero, a join walks the
 // segments of a head (S <- decay S + segment's state), and a second pass starts each
 // segment from its true state.
+//
+// What bounds it: no more than two blocks fit an SM's registers (one in fp32), and their
+// warps wait for each other's results more than the tensor pipe is busy.  fp32, packed
+// [5003] rows in nine sequences, H12 N64 G4: 143 us, 40 % of the tensor pipe's time and
+// 36 % of the issue slots (three planes of an operand: six products for one).
 #include <type_traits>
 
 #include "scan_common.cuh"
@@ -437,6 +442,8 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanDev a, int ele
 // ---------------------------------------------------------------- single tokens
 // Block = one (sequence, head): N / 4 lanes hold one row of the state, four columns
 // each; every element is read once, updated, used for y and written.  s_out may be s_in.
+// Bound by the states' traffic: B256 H40 N128 (671 MB) 99.9 us, 6.7 TB/s; of one sequence
+// (H32) 2.8 us, a launch and the latency of two dependent loads.
 template <typename IO, int N>
 __global__ void __launch_bounds__(256)
     scan_step_kernel(const IO* __restrict__ x, long ldx, const void* __restrict__ dt, long lddt, int dt_bf16,
@@ -485,9 +492,10 @@ __global__ void __launch_bounds__(256)
 constexpr CutCost kCutWarp{kChunk, 296, 0.5, 1.0, 2.0};
 constexpr CutCost kCutWarpF32{kChunk, 148, 0.5, 1.0, 1.0};
 constexpr CutCost kCutTc{128, 148, 0.5, 1.5, 2.0};
-// bf16 with N = 128 runs on the tcgen05 kernel (its tiles are 128 columns wide; rows are
-// numbered in 31 bits there).
-bool uses_tc(int io_dtype, int N, long rows) { return io_dtype == WKV7_BF16 && N == 128 && rows < (1L << 31); }
+// bf16 with N = 128 runs on the tcgen05 kernel, whose tiles are 128 columns wide: B4 T1024 H32
+// takes 35 us there and took 114 on this file's.  Smaller N would leave those tiles half
+// empty or more, and fp32 rows would be three planes of each operand in its shared memory.
+bool uses_tc(int io_dtype, int N) { return io_dtype == WKV7_BF16 && N == 128; }
 
 template <typename IO, int N>
 cudaError_t scan_typed(const ScanArgs& p, const SegMap& map, bool whole, ScanDev& d, cudaStream_t st) {
@@ -567,7 +575,7 @@ size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
 
 cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
     const bool packed = p.seq_offsets != nullptr;
-    const bool tc = uses_tc(io_dtype, p.N, packed ? p.T : static_cast<long>(p.B) * p.T);
+    const bool tc = uses_tc(io_dtype, p.N);
     const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, packed, tc ? kCutTc : io_dtype == WKV7_BF16 ? kCutWarp : kCutWarpF32);
     const bool whole = map.seg >= p.T;
     uint8_t* ws = static_cast<uint8_t*>(p.ws);
@@ -594,8 +602,7 @@ cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
     if (io_dtype == WKV7_BF16) switch (p.N) {
             case 16: return scan_typed<__nv_bfloat16, 16>(p, map, whole, d, stream);
             case 32: return scan_typed<__nv_bfloat16, 32>(p, map, whole, d, stream);
-            case 64: return scan_typed<__nv_bfloat16, 64>(p, map, whole, d, stream);
-            default: return scan_typed<__nv_bfloat16, 128>(p, map, whole, d, stream);
+            default: return scan_typed<__nv_bfloat16, 64>(p, map, whole, d, stream);
         }
     switch (p.N) {
         case 16: return scan_typed<float, 16>(p, map, whole, d, stream);

@@ -16,12 +16,17 @@
 // tokens that act on each other.  Last, d delta_s has the term
 // x_s . (sum G L dy + e dS B_s), and d softplus(u) / du = 1 - exp(-softplus(u)).
 //
-// Launches: the decays; (1) the states S_0 and the gradients dS at every chunk boundary, forwards
-// and backwards side by side, written as bf16 planes (over segments where sequences
-// and heads are few, as in wkv7_scan.cu; on tcgen05 in wkv7_scan_tc.cu for bf16 and N = 128); (2) one block per chunk, group and share of
+// Launches: the decays; (1) the states S_0 and the gradients dS at every chunk boundary,
+// forwards and backwards side by side, written as bf16 planes (over segments where
+// sequences and heads are few, as in wkv7_scan.cu; on tcgen05 in wkv7_scan_tc.cu for bf16
+// and N = 128); (2) one block per chunk, group and share of
 // the group's heads, which keeps the sums over heads in registers: warps 0-3 hold 16
 // tokens t each (dC, E, sums over s), warps 4-7 16 tokens s each (dx, dB, F, sums over
 // t); (3) sums over the shares and over chunks, in a fixed order.
+//
+// Measured at B4 T1024 H32 N128 bf16: decays 3.6 us, (1) 49.7, (2) 148, (3) 4.  (2) has eight
+// warps an SM, all their registers in use: tensor pipe 31 %, the rest waits on the chain of
+// products, exponentials and row sums within a warp.
 #include "scan_backward.cuh"
 
 namespace wkv7 {

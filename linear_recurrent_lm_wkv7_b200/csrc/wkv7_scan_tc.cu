@@ -25,6 +25,11 @@
 // Lanes 32 (w % 4) .. of tensor memory belong to warps w, and so does the SM's quarter that
 // they issue on: warps 3 and 7 make four blocks of M, warps 0 and 4 one.  The jobs that
 // touch no tensor memory are therefore put on the first quarters.
+//
+// Measured: B4 T1024 H32 35.3 us (128 blocks of eight chunks), B1 T16384 H40 145 us + 69 for
+// the states of its segments.  Per chunk the products alone take some 3000 cycles of 8000:
+// tensor pipe 31 %, issue slots 45 %; the rest is the chain state -> planes -> (2) -> y, whose
+// warps also round and store, and instructions fetched again (24 warps on six programs).
 #include <cuda.h>
 
 #include "scan_backward.cuh"
@@ -685,11 +690,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // As scan_states_kernel (wkv7_scan_backward.cu): blockIdx.y 0 walks the states forwards from
 // x and B, 1 their gradients backwards from dy and C, in chunks of 64 tokens, and with
 // WRITE leaves each at every chunk.  Product (4) alone, K = 64, with the chunks' decays
-// loaded like the rows.  18 warps: 0-7 the state (lane n, half of p each), 8-15 the scaled
+// loaded like the rows.  19 warps: 0-7 the state (lane n, half of p each), 8-15 the scaled
 // rows in two groups that take pieces of 32 tokens in turn, 16 loads, 17 products, 18 stores.
 // A state leaves as one bulk copy of its 48 KB out of two buffers.  At B4 T1024 H32 (201 MB
-// written) 49.7 us, 4.0 TB/s, 12 % of it an uneven second wave of blocks; 59.9 us with one
-// buffer, 93 us stored from the registers, 74 us in scan_states_kernel's form on mma.sync.
+// written) 49.7 us, 4.0 TB/s: 256 blocks in two waves of 148; 59.9 us with one buffer,
+// 93 us stored from the registers, 74 us in scan_states_kernel's form on mma.sync.
 constexpr int kStStages = 3, kStRing = 4, kStOuts = 2, kStThreads = 19 * 32;
 constexpr uint32_t kStTile = kChunk * 128;  // 64 rows of 128 bytes
 constexpr uint32_t kStStage = 3 * kStTile;

@@ -79,7 +79,9 @@ int scan_check(int64_t B, int64_t T, int64_t H, int D, int N, int G, int io_dtyp
     if (D != kHead || (N != 16 && N != 32 && N != 64 && N != 128)) return WKV7_ERR_UNSUPPORTED;
     // blocks, one or more per (sequence, head) or per (chunk, head), are numbered in 31 bits
     const int64_t slots = (packed ? T / 64 : B * ((T + 63) / 64)) + B;
-    if (H > kMaxChannels || slots >= (int64_t(1) << 31) / H) return WKV7_ERR_UNSUPPORTED;
+    // and so are rows, which no device's memory reaches
+    if (H > kMaxChannels || slots >= (int64_t(1) << 31) / H || (packed ? T : B * T) >= (int64_t(1) << 31))
+        return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
 }
 

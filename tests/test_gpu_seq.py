@@ -7,8 +7,8 @@ eps(t) / 2 of its value.  What goes on inside is a sum of terms, each off by a r
 * fp32 arithmetic: a chain of m additions is off by m 2^-24 at most; m = 64 tokens of a
   chunk + N columns + the number of chunks (scan), W + 2 (convolution), and for sums over
   rows their number.  Exponentials and the sigmoid: 2^-21.
-* the scan's fp32 values as bf16 planes: 2^-17 with two planes (outputs in bf16 alone),
-  2^-23 with three.  Matrix units cut instead of rounding: 2^-23 an addition, so chains
+* the scan's fp32 values as bf16 planes: 2^-16 with two planes (outputs in bf16 alone),
+  none with three.  Matrix units cut instead of rounding: 2^-23 an addition, so chains
   count twice.
 """
 import pytest

@@ -107,6 +107,7 @@ def test_scan_refusals(wk, step):
         assert call(sT=None) == -1
     else:
         assert call(T=-1) == -1 and call(T=(1 << 31) - 1, H=1 << 12, ldx=1 << 18, ldy=1 << 18, lddt=1 << 12) == -2
+        assert call(B=1 << 16, T=1 << 15) == -2  # 2^31 rows
         # a case that works in segments needs its workspace
         need = wk.wkv7_selective_scan_workspace_bytes(1, 20000, 4, 64, 32, False)
         assert need > 0 and call(B=1, T=20000, ws=None) == -1 and call(B=1, T=20000, wsb=need - 1) == -1
