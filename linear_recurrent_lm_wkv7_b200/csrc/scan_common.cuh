@@ -48,7 +48,8 @@ inline __host__ __device__ long seg_slots(const SegMap& m) {
 // How a kernel that carries one head's state through chunks is best cut (wkv7_scan.cu).
 struct CutCost {
     int chunk;       // tokens per chunk
-    int resident;    // blocks that run at once
+    int per_sm;      // blocks that an SM runs at once
+    double share;    // time of a chunk where it does, of a chunk's alone
     double states;   // time of a chunk in the pass that only makes states, of a chunk's otherwise
     double start;    // time before a block's first chunk, in chunks
     double join;     // of the join and the launches, in chunks

@@ -16,11 +16,11 @@
 // segments of a head (S <- decay S + segment's state), and a second pass starts each
 // segment from its true state.
 //
-// What bounds it: no more than two blocks fit an SM's registers (one in fp32), and their
+// What bounds it: no more than two blocks fit an SM, and their
 // warps wait for each other's results more than the tensor pipe is busy.  fp32, packed
-// [5003] rows in nine sequences, H12 N64 G4: 143 us, 40 % of the tensor pipe's time and
-// 36 % of the issue slots (three planes of an operand: six products for one).
-#include <type_traits>
+// [5003] rows in nine sequences, H12 N64 G4: decays 4 us, states 22, join 4, outputs 51, where
+// half of the tensor pipe's time is used (three planes of an operand: six products for one).
+#include <algorithm>
 
 #include "scan_common.cuh"
 
@@ -44,10 +44,18 @@ struct FwdLayout {
     static constexpr int off_m = stages * stage_bytes;
     static constexpr int xchg_bytes = kScanThreads * 16 * 4;
     static constexpr int m_bytes = TM::bytes > xchg_bytes ? TM::bytes : xchg_bytes;
-    static constexpr int off_y = off_m + m_bytes;  // fp32 rows of Y, one area per warp
-    static constexpr int y_pitch = 20;             // floats: 16 rows p of a token and 4 of padding
+    // fp32 rows of Y, one area per warp: over B and C, which have been used by then, where
+    // they are large enough
+    static constexpr int y_pitch = 20;  // floats: 16 rows p of a token and 4 of padding
     static constexpr int y_bytes = sizeof(IO) == 2 ? 0 : 8 * 32 * y_pitch * 4;
-    static constexpr int off_d = off_y + y_bytes;
+    static constexpr bool y_over = 2 * TB::bytes >= y_bytes;
+    static constexpr int off_d = off_m + m_bytes + (y_over ? 0 : y_bytes);
+    static constexpr int off_y = y_over ? TX::bytes : off_m + m_bytes;
+    static_assert(off_y + y_bytes <= off_d, "rows of Y");
+    // Blocks per SM: two where shared memory has room.  (fp32 N = 64 with one block, the
+    // next chunk's rows ahead in registers: 57 us and 23 for the states of the segments,
+    // against 51 and 22; with no more blocks than SMs 112 us against 123.)
+    static constexpr int resident = sizeof(IO) == 2 || N <= 64 ? 2 : 1;
     static constexpr int bytes = off_d + 2 * static_cast<int>(sizeof(Decays));
 };
 
@@ -83,7 +91,8 @@ struct ScanDev {
 // start state is the slot's in seg_state (OUT) or zero (!OUT, which then writes the
 // end state and the decay of the slot).
 template <typename IO, int N, bool OUT>
-__global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_kernel(const ScanDev a, bool whole) {
+__global__ void __launch_bounds__(kScanThreads, FwdLayout<IO, N>::resident)
+    scan_kernel(const ScanDev a, bool whole) {
     using LY = FwdLayout<IO, N>;
     using TX = typename LY::TX;
     using TB = typename LY::TB;
@@ -139,25 +148,8 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
         cp_decays(sb + LY::off_d + (c & 1) * static_cast<uint32_t>(sizeof(Decays)), dg + static_cast<long>(c) * a.H, tid);
         cp_async_commit();
     };
-    // fp32: the next chunk's rows in registers, where they fit (N <= 64)
-    constexpr bool kAhead = LY::stages == 1 && N <= 64;
-    struct Next {
-        TileRegs<kScanP, kScanThreads> x;
-        TileRegs<N, kScanThreads> b, c;
-    };
-    struct None {};
-    std::conditional_t<kAhead, Next, None> nx;
-    auto fetch = [&](int c) {
-        if constexpr (kAhead) {
-            const int nr = count(c);
-            nx.x.fetch(xg + static_cast<long>(c) * kChunk * a.ldx, a.ldx, nr, tid);
-            nx.b.fetch(bg + static_cast<long>(c) * kChunk * a.ldb, a.ldb, nr, tid);
-            if constexpr (OUT) nx.c.fetch(cg + static_cast<long>(c) * kChunk * a.ldc, a.ldc, nr, tid);
-        }
-    };
     if constexpr (LY::stages == 2) load(0);
     load_decays(0);
-    fetch(0);
 
     // state: S[i] = tile of columns n0 + 8 i; rows 16 pg + g8 (0, 1) and + 8 (2, 3)
     float S[NT][4];
@@ -190,19 +182,10 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1) scan_ke
             }
         } else {
             __syncthreads();  // the last chunk's readers are done
-            if constexpr (kAhead) {
-                nx.x.template put<TX>(stage(c), tid);
-                nx.b.template put<TB>(stage(c) + TX::bytes, tid);
-                if constexpr (OUT) nx.c.template put<TB>(stage(c) + TX::bytes + TB::bytes, tid);
-            } else {
-                load(c);
-            }
+            load(c);
             cp_async_wait<0>();
             __syncthreads();
-            if (c + 1 < chunks) {
-                load_decays(c + 1);
-                fetch(c + 1);
-            }
+            if (c + 1 < chunks) load_decays(c + 1);
         }
         const Decays& d = dec[c & 1];
         const uint32_t sx = stage(c), sB = sx + TX::bytes, sC = sB + TB::bytes, sM = sb + LY::off_m;
@@ -486,12 +469,15 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// The kernels: this file's on warp-level products, two blocks per SM in bf16 and one in
-// fp32, and wkv7_scan_tc.cu's.  (At B1 T16384 H40 N128 a chunk of 128 tokens takes the
-// latter 3.8 us with its outputs and 1.8 without.)
-constexpr CutCost kCutWarp{kChunk, 296, 0.5, 1.0, 2.0};
-constexpr CutCost kCutWarpF32{kChunk, 148, 0.5, 1.0, 1.0};
-constexpr CutCost kCutTc{128, 148, 0.5, 1.5, 2.0};
+// The kernels: this file's on warp-level products, one block per SM for fp32 with N = 128
+// and two otherwise, and wkv7_scan_tc.cu's.  (At B1 T16384 H40 N128 a chunk of 128 tokens
+// takes the latter 3.8 us with its outputs and 1.8 without.)
+constexpr CutCost kCutWarp{kChunk, 2, 1.4, 0.5, 0.5, 2.0};
+constexpr CutCost kCutTc{128, 1, 1.0, 0.5, 1.5, 2.0};
+constexpr CutCost kCutWarpF32{kChunk, 2, 1.7, 0.5, 0.5, 1.0}, kCutWarpF32Large{kChunk, 1, 1.0, 0.5, 1.0, 1.0};  // large: N = 128
+const CutCost& cut_cost(int io_dtype, int N) {
+    return io_dtype == WKV7_BF16 ? N == 128 ? kCutTc : kCutWarp : N == 128 ? kCutWarpF32Large : kCutWarpF32;
+}
 // bf16 with N = 128 runs on the tcgen05 kernel, whose tiles are 128 columns wide: B4 T1024 H32
 // takes 35 us there and took 114 on this file's.  Smaller N would leave those tiles half
 // empty or more, and fp32 rows would be three planes of each operand in its shared memory.
@@ -517,25 +503,32 @@ cudaError_t scan_typed(const ScanArgs& p, const SegMap& map, bool whole, ScanDev
 
 }  // namespace
 
-// Sequences are cut into S segments where that is faster: blocks of one segment each run
-// in waves, and a cut needs a pass over the states and the join first.
+// Sequences are cut into segments where that is faster: blocks of one segment each run in
+// waves, and a cut needs a pass over the states and the join first.  Of packed sequences
+// only the mean length is known here; the longest is taken to have twice that.  (fp32
+// packed [5003] rows in nine sequences, H12 N64: 80 us in segments of four chunks, 145 whole.
+// bf16 B4 T1024 H32 N64: 64 us whole, 74 in two segments; B1 T4096 H40 N64: 90 us in seven,
+// 115 in three.)
 SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed, const CutCost& k) {
     SegMap m{offs, B, T, 0, 1};
-    const long per = packed ? (T + B - 1) / B : T, units = static_cast<long>(B) * H;
-    const long chunks = (per + k.chunk - 1) / k.chunk;
-    auto waves = [&](long blocks) { return static_cast<double>((blocks + k.resident - 1) / k.resident); };
+    const long total = (static_cast<long>(T) + k.chunk - 1) / k.chunk, units = static_cast<long>(B) * H;
+    const long mean = packed ? (total + B - 1) / B : total, chunks = std::min(total, packed && B > 1 ? 2 * mean : mean);
+    const long sms = 148, resident = sms * k.per_sm;
+    const auto waves = [&](long blocks) { return blocks <= sms ? 1.0 : (blocks + resident - 1) / resident * k.share; };
     long best = 1;
-    double least = waves(units) * (chunks + k.start);
-    for (long s = 2; s <= chunks && s <= 64 && units * s <= 8L * k.resident; ++s) {
+    double least = std::max(waves(units) * (mean + k.start), chunks + k.start);
+    for (long s = 2; s <= chunks && s <= 64 && units * s <= 8 * resident; ++s) {
         const long c = (chunks + s - 1) / s;
-        const double t = waves(units * s) * (c * (1.0 + k.states) + 2 * k.start) + k.join;
+        // half of the sequences' last segments count as full ones
+        const double w = waves(packed ? (2 * total + c * B) * H / (2 * c) : units * s);
+        const double t = w * (c * (1.0 + k.states) + 2 * k.start) + k.join;
         if (t < least) {
             least = t;
             best = s;
         }
     }
     if (best == 1) {
-        m.seg = (static_cast<long>(T) + k.chunk - 1) / k.chunk * k.chunk;
+        m.seg = total * k.chunk;
         if (m.seg == 0) m.seg = k.chunk;
         return m;
     }
@@ -567,16 +560,15 @@ static size_t decays_bytes(int B, int T, int H, bool packed) {
     return static_cast<size_t>(chunk_slots(B, T, packed)) * H * sizeof(Decays);
 }
 size_t scan_workspace_bytes(int B, int T, int H, int N, bool packed) {
-    const size_t b = cut_floats(B, T, H, N, packed, kCutWarp), f = cut_floats(B, T, H, N, packed, kCutWarpF32);
-    const size_t w = (b > f ? b : f) * sizeof(float) + decays_bytes(B, T, H, packed);
-    const size_t t = N == 128 ? cut_floats(B, T, H, N, packed, kCutTc) * sizeof(float) : 0;
-    return w > t ? w : t;
+    const size_t b = cut_floats(B, T, H, N, packed, cut_cost(WKV7_BF16, N));
+    const size_t f = cut_floats(B, T, H, N, packed, cut_cost(WKV7_F32, N));
+    return (b > f ? b : f) * sizeof(float) + decays_bytes(B, T, H, packed);
 }
 
 cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
     const bool packed = p.seq_offsets != nullptr;
     const bool tc = uses_tc(io_dtype, p.N);
-    const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, packed, tc ? kCutTc : io_dtype == WKV7_BF16 ? kCutWarp : kCutWarpF32);
+    const SegMap map = scan_segments(p.B, p.T, p.H, p.seq_offsets, packed, cut_cost(io_dtype, p.N));
     const bool whole = map.seg >= p.T;
     uint8_t* ws = static_cast<uint8_t*>(p.ws);
     Decays* dec = reinterpret_cast<Decays*>(ws);

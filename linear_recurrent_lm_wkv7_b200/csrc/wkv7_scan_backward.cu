@@ -893,8 +893,8 @@ struct Plan {
 Plan plan_of(int B, int T, int H, int N, int G, int io_dtype, const int32_t* offs, bool packed) {
     Plan p;
     // both directions run at once; without segments the one pass makes states anyway
-    const int resident = io_dtype == WKV7_BF16 && N != 128 ? 296 : 148;
-    p.seg = scan_segments(B, T, 2 * H, offs, packed, CutCost{kChunk, resident, 1.0, 1.0, 2.0});
+    p.seg = scan_segments(B, T, 2 * H, offs, packed, io_dtype == WKV7_BF16 && N != 128 ? CutCost{kChunk, 2, 1.4, 1.0, 1.0, 2.0}
+                                                        : CutCost{kChunk, 1, 1.0, 1.0, 1.0, 2.0});
     p.whole = p.seg.seg >= T;
     p.chunk = chunk_map(B, T, offs);
     p.seg_count = packed ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;
