@@ -273,7 +273,8 @@ struct GradLayout {
     static constexpr int off_d = off_c + TB::bytes;
     static constexpr int off_sc = off_d + 3 * static_cast<int>(sizeof(Decays));  // the last head's until its end
     static constexpr int sc_floats = 7 * kChunk + 16;  // per head, twice
-    static constexpr int bytes = off_sc + 2 * sc_floats * 4;
+    static constexpr int off_x = off_sc + 2 * sc_floats * 4;  // half of e dS B, by fragments
+    static constexpr int bytes = off_x + 4 * 4 * 32 * 16;
 };
 static_assert(GradLayout<__nv_bfloat16, 128>::bytes <= 227 * 1024 && GradLayout<float, 128>::bytes <= 227 * 1024,
               "shared memory of an SM");
@@ -578,24 +579,50 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             dot = warp_sum(dot);
             if (lane == 0) hs.dot[warp] = dot;
         }
-        float X[8][4];  // s side: dx.  First e dS B
+        // ---- e dS B, the first part of dx: the s side takes 32 columns p, the t side (which has
+        // no product with dS of its own) the others, and hands them over
+        float X[8][4];
+        {
+            const int p0 = s_side ? 0 : 32;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) X[j][0] = X[j][1] = X[j][2] = X[j][3] = 0.f;
-        if (s_side) {
+            for (int j = 0; j < 8; ++j) X[j][0] = X[j][1] = X[j][2] = X[j][3] = 0.f;
 #pragma unroll
             for (int k = 0; k < N; k += 16) {
                 uint32_t fa[PI][4];
                 frag_a<TB>(fa, sb + LY::off_b, blk * 16, k, lane);
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
+                for (int j = 0; j < 4; j += 2) {
                     uint32_t fb[2][kStatePlanes][2];
                     if constexpr (LY::transposed)
-                        frag_b_t<TS>(fb, sb + ods, j * 8, k, lane);
+                        frag_b_t<TS>(fb, sb + ods, p0 + j * 8, k, lane);
                     else
-                        frag_b<TS>(fb, sb + ods, j * 8, k, lane);
+                        frag_b<TS>(fb, sb + ods, p0 + j * 8, k, lane);
                     mma_planes<PI, kStatePlanes>(X[j], fa, fb[0]);
                     mma_planes<PI, kStatePlanes>(X[j + 1], fa, fb[1]);
                 }
+            }
+        }
+        float4* xc = reinterpret_cast<float4*>(smem + LY::off_x) + blk * 4 * 32 + lane;
+        if (s_side) {
+            const float scale[2] = {d.to[row0] * d.delta[row0], d.to[row0 + 8] * d.delta[row0 + 8]};
+            float unused[2];
+            times_state(ox, ods, scale, unused);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xc[j * 32] = make_float4(X[j][0], X[j][1], X[j][2], X[j][3]);
+        }
+        __syncthreads();  // the states have been used, e dS B is complete
+        if constexpr (LY::stages == 2) {
+            if (i + 1 < heads) {
+                load(i + 1);
+                load_states(i + 1);
+            }
+        }
+        if (s_side) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 v = xc[j * 32];
+                X[4 + j][0] = v.x, X[4 + j][1] = v.y, X[4 + j][2] = v.z, X[4 + j][3] = v.w;
             }
             float fs[2] = {0.f, 0.f};
 #pragma unroll
@@ -611,18 +638,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
                 fs[r] = quad_sum(fs[r]);
                 if ((lane & 3) == 0) hs.f[row0 + 8 * r] = fs[r];
             }
-            const float scale[2] = {d.to[row0] * d.delta[row0], d.to[row0 + 8] * d.delta[row0 + 8]};
-            float unused[2];
-            times_state(ox, ods, scale, unused);
         }
-        if constexpr (LY::stages == 2) {
-            __syncthreads();  // the states have been used
-            if (i + 1 < heads) {
-                load(i + 1);
-                load_states(i + 1);
-            }
-        }
-
         // ---- M (t side) or its transpose, and everything that is made of it
         float M[8][4];
 #pragma unroll
