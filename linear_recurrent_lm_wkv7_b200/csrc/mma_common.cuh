@@ -131,6 +131,21 @@ struct Tile {
     static constexpr int plane = ROWS * pitch;
     static constexpr int bytes = PLANES * plane;
     static constexpr int planes = PLANES;
+    __device__ static __forceinline__ uint32_t at(int row, int col) { return row * pitch + col * 2; }
+};
+// The same without padding, as one contiguous copy brings it: row r holds its 16-byte pieces
+// at their index xor a number that differs between rows of the same banks.
+template <int PLANES, int ROWS, int COLS>
+struct SwizzledTile {
+    static constexpr int pitch = COLS * 2;
+    static constexpr int plane = ROWS * pitch;
+    static constexpr int bytes = PLANES * plane;
+    static constexpr int planes = PLANES;
+    static constexpr int pieces = COLS / 8, per_line = pitch < 128 ? 128 / pitch : 1;
+    __host__ __device__ static constexpr int swizzle(int row) { return row / per_line & (pieces < 8 ? pieces - 1 : 7); }
+    __device__ static __forceinline__ uint32_t at(int row, int col) {
+        return row * pitch + (col * 2 ^ swizzle(row) * 16);
+    }
 };
 
 // Lane addresses of the four 8x8 blocks of a 16 x 16 piece at (row, col) of a tile:
@@ -138,13 +153,13 @@ struct Tile {
 // row-major A, or with `t` (transposing load) of an A stored [k][m], where row is k.
 template <typename TL>
 __device__ __forceinline__ uint32_t addr_a(uint32_t base, int row, int col, int lane) {
-    return base + (row + (lane & 15)) * TL::pitch + (col + (lane >> 4) * 8) * 2;
+    return base + TL::at(row + (lane & 15), col + (lane >> 4) * 8);
 }
 // Order (0,0) (0,8) (8,0) (8,8): two n-tiles' B fragments (k 0-7 and 8-15 of rows
 // n 0-7, then of rows n 8-15) from a B stored [n][k].
 template <typename TL>
 __device__ __forceinline__ uint32_t addr_b(uint32_t base, int row, int col, int lane) {
-    return base + (row + (lane & 7) + (lane >> 4) * 8) * TL::pitch + (col + ((lane >> 3) & 1) * 8) * 2;
+    return base + TL::at(row + (lane & 7) + (lane >> 4) * 8, col + ((lane >> 3) & 1) * 8);
 }
 
 // A fragments [m 16][k 16] of a tile stored [m][k].

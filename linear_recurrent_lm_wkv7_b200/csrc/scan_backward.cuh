@@ -17,7 +17,7 @@ struct BwdDev {
     long seg_count, chunk_count;
     // workspace
     const Decays* dec;      // [chunk][H]
-    __nv_bfloat16* states;  // [2][chunk][H][plane][64][N] (or [N][64], kStatesT): S_0 and dS
+    __nv_bfloat16* states;  // [2][chunk][H] StateTile: S_0 and dS
     float* seg_state;       // [2][seg][H][64][N]
     float* seg_decay;       // [seg][H]
     float* part;            // [2][share][row][G N]: dB and dC of a share of the heads
@@ -27,10 +27,12 @@ struct BwdDev {
     int* status;
 };
 
-// The tcgen05 kernel holds a state column per lane and writes the states transposed, as
-// they lie in its shared memory: the 16-byte pieces of row n at their index xor n mod 8.
+// The tcgen05 kernel holds a state column per lane and writes the states transposed.
 template <typename IO, int N>
 constexpr bool kStatesT = sizeof(IO) == 2 && N == 128;
+// A state as it lies in memory, and in shared memory after one bulk copy.
+template <typename IO, int N>
+using StateTile = SwizzledTile<kStatePlanes, kStatesT<IO, N> ? N : kScanP, kStatesT<IO, N> ? kScanP : N>;
 
 // One pass of the states in both directions on tcgen05: as scan_states_kernel.
 cudaError_t launch_states_tc(const BwdDev& d, bool write, bool whole, cudaStream_t stream);

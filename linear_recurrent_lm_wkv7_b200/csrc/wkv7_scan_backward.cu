@@ -28,6 +28,7 @@
 // warps an SM, all their registers in use: tensor pipe 31 %, the rest waits on the chain of
 // products, exponentials and row sums within a warp.
 #include "scan_backward.cuh"
+#include "sm100_ptx.cuh"
 
 namespace wkv7 {
 namespace {
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
                                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                  : "r"(so + r * TO::pitch + c * 16)
                                  : "memory");
-                    *reinterpret_cast<uint4*>(dst + p * kState + (pg * 16 + r) * N + n0 + c * 8) = v;
+                    *reinterpret_cast<uint4*>(dst + p * kState + StateTile<IO, N>::at(pg * 16 + r, n0 + c * 8) / 2) = v;
                 }
             }
         }
@@ -260,8 +261,7 @@ struct GradLayout {
     using TX = Tile<PI, kChunk, kScanP>;
     using TB = Tile<PI, kChunk, N>;
     static constexpr bool transposed = kStatesT<IO, N>;
-    static constexpr int s_rows = transposed ? N : kScanP, s_cols = transposed ? kScanP : N;
-    using TS = Tile<kStatePlanes, s_rows, s_cols>;
+    using TS = StateTile<IO, N>;
     // bf16: the next head's rows of x and dy are copied while this one is worked on, its
     // states once this one's have been used.  fp32: one stage, in which S_0 and dS take
     // turns in one place.
@@ -274,7 +274,8 @@ struct GradLayout {
     static constexpr int off_sc = off_d + 3 * static_cast<int>(sizeof(Decays));  // the last head's until its end
     static constexpr int sc_floats = 7 * kChunk + 16;  // per head, twice
     static constexpr int off_x = off_sc + 2 * sc_floats * 4;  // half of e dS B, by fragments
-    static constexpr int bytes = off_x + 4 * 4 * 32 * 16;
+    static constexpr int off_bar = off_x + 4 * 4 * 32 * 16;
+    static constexpr int bytes = off_bar + 16;
 };
 static_assert(GradLayout<__nv_bfloat16, 128>::bytes <= 227 * 1024 && GradLayout<float, 128>::bytes <= 227 * 1024,
               "shared memory of an SM");
@@ -367,25 +368,38 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
     const IO* yg = static_cast<const IO*>(a.dy) + r0 * a.lddy;
 
     auto stage = [&](int i) { return (i % LY::stages) * LY::stage_bytes; };
+    // The states come by bulk copies, the rows by every thread's own (16 bytes each, the
+    // states took 2500 of a head's 16000 cycles, N = 128).
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + LY::off_bar);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
     auto load_state = [&](int off, int back, int h) {
-        const __nv_bfloat16* src = a.states + (((back ? a.chunk_count : 0) + slot) * a.H + h) * (kStatePlanes * kState);
-        constexpr int per = LY::s_cols / 8;
-        for (int i = tid; i < kStatePlanes * LY::s_rows * per; i += kScanThreads) {
-            const int r = i / per, c = i % per;
-            const int to = LY::transposed ? c ^ (r & 7) : c;  // planes follow each other
-            cp_async16(sb + off + r * TS::pitch + to * 16, src + i * 8, true);
+        bulk_load(smem + off, a.states + (((back ? a.chunk_count : 0) + slot) * a.H + h) * (kStatePlanes * kState),
+                  TS::bytes, bar);
+    };
+    bool ok = true;  // a wait that gives up is reported, and is the last
+    uint32_t phase = 0;
+    auto wait_states = [&]() {
+        if (ok && !mbar_wait(bar, phase & 1, 2000000000ull)) {
+            ok = false;
+            report_status(a.status, WKV7_ERR_DEVICE_TIMEOUT);
         }
+        ++phase;
     };
     auto load = [&](int i) {
         const int h = h0 + i, s = stage(i);
         load_tile<TX, kScanP>(sb + s, xg + h * kScanP, a.ldx, nr, tid, kScanThreads);
         load_tile<TX, kScanP>(sb + s + TX::bytes, yg + h * kScanP, a.lddy, nr, tid, kScanThreads);
         cp_decays(sb + LY::off_d + (i % 3) * static_cast<uint32_t>(sizeof(Decays)), a.dec + slot * a.H + h, tid);
+        cp_async_commit();
     };
     auto load_states = [&](int i) {
+        if (tid != 0) return;
+        mbar_arrive_expect_tx(bar, (LY::shared_state ? 1 : 2) * TS::bytes);
         load_state(LY::off_s0, 0, h0 + i);
         if constexpr (!LY::shared_state) load_state(LY::off_ds, 1, h0 + i);
-        cp_async_commit();
     };
     auto sums = [&](int i) {
         float* p = reinterpret_cast<float*>(smem + LY::off_sc) + (i & 1) * LY::sc_floats;
@@ -485,6 +499,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             cp_async_wait<0>();
             __syncthreads();
         }
+        wait_states();
         const Decays& d = dec[i % 3];
         const HeadSums hs = sums(i);
         const int ox = stage(i), oy = ox + TX::bytes;
@@ -540,10 +555,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
         }
         if constexpr (LY::shared_state) {
             __syncthreads();  // S_0 has been read
-            load_state(ods, 1, h0 + i);
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncthreads();
+            if (tid == 0) {
+                mbar_arrive_expect_tx(bar, TS::bytes);
+                load_state(ods, 1, h0 + i);
+            }
+            wait_states();
         }
         // ---- <S_0, dS>
         {
@@ -551,17 +567,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
             const __nv_bfloat16* g = a.states + (slot * a.H + h0 + i) * (kStatePlanes * kState);
 #pragma unroll
             for (int k = 0; k < kState / 8 / kScanThreads + (kState / 8 % kScanThreads ? 1 : 0); ++k) {
-                const int p = tid + k * kScanThreads;
+                const int p = tid + k * kScanThreads;  // eight columns of a row
                 if (kState / 8 % kScanThreads && p >= kState / 8) continue;
-                const int r = p / (LY::s_cols / 8), c = p % (LY::s_cols / 8) * 8;  // eight columns of a row
                 uint4 u[kStatePlanes], v[kStatePlanes];
 #pragma unroll
                 for (int w = 0; w < kStatePlanes; ++w) {
-                    u[w] = *reinterpret_cast<const uint4*>(smem + ods + w * TS::plane + r * TS::pitch + c * 2);
+                    u[w] = *reinterpret_cast<const uint4*>(smem + ods + w * TS::plane + p * 16);
                     if constexpr (LY::shared_state)
-                        v[w] = *reinterpret_cast<const uint4*>(g + w * kState + r * LY::s_cols + c);
+                        v[w] = *reinterpret_cast<const uint4*>(g + w * kState + p * 8);
                     else
-                        v[w] = *reinterpret_cast<const uint4*>(smem + os0 + w * TS::plane + r * TS::pitch + c * 2);
+                        v[w] = *reinterpret_cast<const uint4*>(smem + os0 + w * TS::plane + p * 16);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
