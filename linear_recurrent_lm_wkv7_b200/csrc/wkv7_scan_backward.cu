@@ -24,8 +24,10 @@
 // tokens t each (dC, E, sums over s), warps 4-7 16 tokens s each (dx, dB, F, sums over
 // t); (3) sums over the shares and over chunks, in a fixed order.
 //
-// Measured at B4 T1024 H32 N128 bf16: decays 3.6 us, (1) 49.7, (2) 148, (3) 4.  (2) has eight
-// warps an SM, all their registers in use: tensor pipe 31 %, the rest waits on the chain of
+// Measured at B4 T1024 H32 N128 bf16: decays 3.6 us, (1) 49.7, (2) 133, (3) 4.  (2) has eight
+// warps an SM, all their registers in use.  Half of a head's 14000 cycles are the products
+// with the states, which shared memory bounds (every warp of a side reads the whole state in
+// three planes, 7700 of the cycles; the tensor pipe is busy for 5500); the rest is the chain of
 // products, exponentials and row sums within a warp.
 #include "scan_backward.cuh"
 #include "sm100_ptx.cuh"
