@@ -104,6 +104,27 @@ __device__ __forceinline__ float act_grad_f32(float x, int act) {
     return s * (1.f + x * (1.f - s));
 }
 
+// ---------------------------------------------------------------- launches of one call
+// A call's second and later kernels are launched while the one before still runs, so that
+// the way to their start is over when it ends.  Each begins with chain_wait, for every
+// thread of every block: it returns when the kernel before has completed (and with it all
+// before that one).  chain_next, in the kernel before, lets the next one come.  A call's first
+// kernel is launched plainly, and so starts when all that the stream holds has ended.
+// (Four kernels of a packed fp32 scan, 5003 rows of H12 N64: 88 us in plain launches, 82 so.)
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                        const A&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = stream;
+    c.attrs = &attr, c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kern, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- packed sequences
 // Start and end row of sequence n of B.  `offs` null: dense sequences of T rows.
 // Packed offsets that are not monotone or leave [0, T] give an empty sequence and

@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     IO* __restrict__ dx, long lddx, IO* __restrict__ ds0, float* __restrict__ part,
                     const int32_t* __restrict__ offs, int B, int T, long rows, int C, int act, int strip_rows,
                     unsigned row_blocks, int* status) {
+    chain_next();
     const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
     const int c = (blockIdx.y * kLanes + lane) * VEC;
     const bool live = c < C;
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 __global__ void __launch_bounds__(kThreads)
     conv_bwd_sum_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ dbias, long nblk,
                         int C, int W) {
+    chain_wait();
     __shared__ float red[kStrips][kLanes];
     const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
     const long cols = static_cast<long>(W + 1) * C, col = static_cast<long>(blockIdx.x) * kLanes + lane;
@@ -494,8 +496,8 @@ cudaError_t bwd_typed(const ConvBwdArgs& p, cudaStream_t st) {
             static_cast<IO*>(p.ds0), p.ws, p.seq_offsets, p.B, p.T, rows, p.C, p.act, kBwdStripRows,
             static_cast<unsigned>(nblk), p.status);
     const long cols = static_cast<long>(W + 1) * p.C;
-    conv_bwd_sum_kernel<<<static_cast<unsigned>((cols + kLanes - 1) / kLanes), kThreads, 0, st>>>(p.ws, p.dw, p.dbias,
-                                                                                                   nblk, p.C, W);
+    launch_next(conv_bwd_sum_kernel, static_cast<unsigned>((cols + kLanes - 1) / kLanes), kThreads, 0, st, p.ws, p.dw,
+                p.dbias, nblk, p.C, W);
     return cudaGetLastError();
 }
 

@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads)
                         const float* __restrict__ bias, const float* __restrict__ stats, const IO* __restrict__ dy,
                         long lddy, IO* __restrict__ dx, long lddx, float* __restrict__ part, long N, int G, int Cg,
                         int gpb, int act) {
+    chain_next();
     __shared__ float red[TEAM > 32 ? TEAM / 32 : 1];
     __shared__ float sums[kThreads * VEC];
     const RowPlace p = row_place<TEAM>(gpb, G);
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(1024)
     norm_sum_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db, long nblk,
                     long C) {
+    chain_wait();
     __shared__ float red[32][33];
     const int lane = threadIdx.x % 32, sub = threadIdx.x / 32;
     const long col = static_cast<long>(blockIdx.x) * 32 + lane;
@@ -275,6 +277,7 @@ template <typename IO, int VEC>
 __global__ void __launch_bounds__(kThreads)
     norm_stats_kernel(const IO* __restrict__ x, long ldx, float* __restrict__ part, long L, int C, int Cg, int lanes,
                       int splits, long split_rows) {
+    chain_next();
     __shared__ Moments mom[kThreads];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
     const int c0 = blockIdx.y * lanes * VEC, c = c0 + lane * VEC;
@@ -367,6 +370,8 @@ __device__ __forceinline__ float2 join_moments(const float* part, long n, int g,
 __global__ void __launch_bounds__(kThreads)
     norm_join_kernel(const float* __restrict__ part, float* __restrict__ stats, long units, int G, int Cg, int splits,
                      int tiles, int tile_c, float eps) {
+    chain_wait();
+    chain_next();
     const long u = static_cast<long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
     if (u >= units) return;
     const float2 s = join_moments(part, u / G, static_cast<int>(u % G), G, Cg, splits, tiles, tile_c, eps,
@@ -382,6 +387,7 @@ __global__ void __launch_bounds__(kThreads)
     norm_apply_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ weight,
                       const float* __restrict__ bias, float* __restrict__ stats, IO* __restrict__ y, long ldy, long L,
                       int C, int Cg, int lanes, int splits, long split_rows, int act, const float* __restrict__ part, float eps) {
+    chain_wait();
     __shared__ float2 joined[JOIN ? kThreads * VEC : 1];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
     const int c0 = blockIdx.y * lanes * VEC, c = c0 + lane * VEC, G = C / Cg;
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(kThreads)
                          const float* __restrict__ bias, const float* __restrict__ stats, const IO* __restrict__ dy,
                          long lddy, float* __restrict__ part, long L, int C, int Cg, int lanes, int splits, long split_rows,
                          int act) {
+    chain_next();
     __shared__ float sums[2][kThreads * VEC];
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
     const int c = (blockIdx.y * lanes + lane) * VEC;
@@ -476,6 +483,8 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     norm_bwd_join_kernel(const float* __restrict__ part, const float* __restrict__ weight, float* __restrict__ mom,
                          long L, int G, int Cg, int splits) {
+    chain_wait();
+    chain_next();
     __shared__ float red[kThreads / 32];
     const long u = blockIdx.x, n = u / G, C = static_cast<long>(G) * Cg;
     const int g = static_cast<int>(u % G);
@@ -502,6 +511,8 @@ __global__ void __launch_bounds__(kThreads)
                           const float* __restrict__ bias, const float* __restrict__ stats,
                           const float* __restrict__ mom, const IO* __restrict__ dy, long lddy, IO* __restrict__ dx,
                           long lddx, long L, int C, int Cg, int lanes, int splits, long split_rows, int act) {
+    chain_wait();
+    chain_next();
     const int par = kThreads / lanes, lane = threadIdx.x % lanes, prow = threadIdx.x / lanes;
     const int c = (blockIdx.y * lanes + lane) * VEC;
     if (prow >= par || c >= C) return;
@@ -632,15 +643,14 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
     // launch for the join).
     const int tile_groups = (s.lanes * VEC + Cg - 1) / Cg + 1;
     if (static_cast<long>(tile_groups) * s.splits * ((Cg + s.lanes * VEC - 1) / (s.lanes * VEC) + 1) <= kJoinMost) {
-        norm_apply_kernel<IO, VEC, true><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, y, p.ldy, p.L,
-                                                                    p.C, Cg, s.lanes, s.splits, s.split_rows, p.act, part,
-                                                                    p.eps);
+        launch_next(norm_apply_kernel<IO, VEC, true>, grid, kThreads, 0, st, x, p.ldx, p.weight, p.bias, p.stats, y, p.ldy, p.L,
+                    p.C, Cg, s.lanes, s.splits, s.split_rows, p.act, part,
+                    p.eps);
     } else {
-        norm_join_kernel<<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, st>>>(
-            part, stats, units, p.G, Cg, s.splits, s.tiles, s.lanes * VEC, p.eps);
-        norm_apply_kernel<IO, VEC, false><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, stats, y, p.ldy, p.L,
-                                                                     p.C, Cg, s.lanes, s.splits, s.split_rows, p.act, nullptr,
-                                                                     p.eps);
+        launch_next(norm_join_kernel, static_cast<unsigned>((units + 7) / 8), kThreads, 0, st, part, stats, units, p.G, Cg, s.splits, s.tiles, s.lanes * VEC, p.eps);
+        launch_next(norm_apply_kernel<IO, VEC, false>, grid, kThreads, 0, st, x, p.ldx, p.weight, p.bias, stats, y, p.ldy, p.L,
+                    p.C, Cg, s.lanes, s.splits, s.split_rows, p.act, nullptr,
+                    p.eps);
     }
     return cudaGetLastError();
 }
@@ -671,14 +681,13 @@ cudaError_t norm_bwd_typed(const NormBwdArgs& p, cudaStream_t st) {
         const dim3 grid(static_cast<unsigned>(p.N) * s.splits, s.tiles);
         norm_bwd_sums_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, dy, p.lddy,
                                                                  p.ws, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows, p.act);
-        norm_bwd_join_kernel<<<static_cast<unsigned>(static_cast<long>(p.N) * p.G), kThreads, 0, st>>>(
-            p.ws, p.weight, mom, p.L, p.G, Cg, s.splits);
-        norm_bwd_apply_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, p.weight, p.bias, p.stats, mom, dy,
-                                                                  p.lddy, dx, p.lddx, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows, p.act);
+        launch_next(norm_bwd_join_kernel, static_cast<unsigned>(static_cast<long>(p.N) * p.G), kThreads, 0, st, p.ws, p.weight, mom, p.L, p.G, Cg, s.splits);
+        launch_next(norm_bwd_apply_kernel<IO, VEC>, grid, kThreads, 0, st, x, p.ldx, p.weight, p.bias, p.stats, mom, dy,
+                    p.lddy, dx, p.lddx, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows, p.act);
     }
     if (p.dw || p.db)
-        norm_sum_kernel<<<static_cast<unsigned>((2L * p.C + 31) / 32), 1024, 0, st>>>(p.ws, p.dw, p.db, nblk,
-                                                                                          p.C);
+        launch_next(norm_sum_kernel, static_cast<unsigned>((2L * p.C + 31) / 32), 1024, 0, st, p.ws, p.dw, p.db, nblk,
+                    p.C);
     return cudaGetLastError();
 }
 

@@ -60,6 +60,7 @@ struct FwdLayout {
 };
 
 __global__ void __launch_bounds__(256) decays_kernel(const DecayArgs a) {
+    chain_next();
     const long u = static_cast<long>(blockIdx.x) * 8 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     if (u >= seg_slots(a.map) * a.H) return;
@@ -93,6 +94,8 @@ struct ScanDev {
 template <typename IO, int N, bool OUT>
 __global__ void __launch_bounds__(kScanThreads, FwdLayout<IO, N>::resident)
     scan_kernel(const ScanDev a, bool whole) {
+    chain_wait();
+    if constexpr (!OUT) chain_next();
     using LY = FwdLayout<IO, N>;
     using TX = typename LY::TX;
     using TB = typename LY::TB;
@@ -392,6 +395,8 @@ __global__ void __launch_bounds__(kScanThreads, FwdLayout<IO, N>::resident)
 // Start states of the segments from their end states (from zero) and decays, in place,
 // and the final states: thread = 4 elements of a head's state, walking its segments.
 __global__ void __launch_bounds__(256) scan_join_kernel(const ScanDev a, int elems) {
+    chain_wait();
+    chain_next();
     const int h = blockIdx.x % a.H;
     const long n = blockIdx.x / a.H;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
@@ -493,11 +498,11 @@ cudaError_t scan_typed(const ScanArgs& p, const SegMap& map, bool whole, ScanDev
     if (!whole) {
         e = configure_smem_once(scan_kernel<IO, N, false>, LY::bytes, cfg_state);
         if (e != cudaSuccess) return e;
-        scan_kernel<IO, N, false><<<grid, kScanThreads, LY::bytes, st>>>(d, false);
+        launch_next(scan_kernel<IO, N, false>, grid, kScanThreads, LY::bytes, st, d, false);
         constexpr int elems = kScanP * N;
-        scan_join_kernel<<<dim3(static_cast<unsigned>(p.B) * p.H, (elems / 4 + 255) / 256), 256, 0, st>>>(d, elems);
+        launch_next(scan_join_kernel, dim3(static_cast<unsigned>(p.B) * p.H, (elems / 4 + 255) / 256), 256, 0, st, d, elems);
     }
-    scan_kernel<IO, N, true><<<grid, kScanThreads, LY::bytes, st>>>(d, whole);
+    launch_next(scan_kernel<IO, N, true>, grid, kScanThreads, LY::bytes, st, d, whole);
     return cudaGetLastError();
 }
 
@@ -583,7 +588,7 @@ cudaError_t launch_scan(const ScanArgs& p, int io_dtype, cudaStream_t stream) {
             e = launch_scan_tc(p, map, false, false, seg_state, seg_decay, stream);
             if (e != cudaSuccess) return e;
             constexpr int elems = kScanP * 128;
-            scan_join_kernel<<<dim3(static_cast<unsigned>(p.B) * p.H, elems / 4 / 256), 256, 0, stream>>>(d, elems);
+            launch_next(scan_join_kernel, dim3(static_cast<unsigned>(p.B) * p.H, elems / 4 / 256), 256, 0, stream, d, elems);
         }
         return launch_scan_tc(p, map, whole, true, seg_state, seg_decay, stream);
     }

@@ -56,6 +56,8 @@ struct StateLayout {
 template <typename IO, int N, bool WRITE>
 __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
     scan_states_kernel(const BwdDev a, bool whole) {
+    chain_wait();
+    chain_next();
     using LY = StateLayout<IO, N>;
     using TX = typename LY::TX;
     using TB = typename LY::TB;
@@ -235,6 +237,8 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
 // The segments' true starts (forwards) and end gradients (backwards, blockIdx.z = 1), in
 // place of what each gives from zero; ds0.
 __global__ void __launch_bounds__(256) scan_states_join_kernel(const BwdDev a, int elems) {
+    chain_wait();
+    chain_next();
     const int h = blockIdx.x % a.H, back = blockIdx.z;
     const long n = blockIdx.x / a.H;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
@@ -336,6 +340,8 @@ __device__ __forceinline__ void store_dt(void* p, long i, float v, bool bf16) {
 
 template <typename IO, int N>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev a) {
+    chain_wait();
+    chain_next();
     using LY = GradLayout<IO, N>;
     using TX = typename LY::TX;
     using TB = typename LY::TB;
@@ -856,6 +862,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
 // The H blocks after them: dA, d dt_bias and dD of a head from its chunks.
 template <typename IO>
 __global__ void __launch_bounds__(256) scan_sum_kernel(const BwdDev a, int width, unsigned sum_blocks) {
+    chain_wait();
     if (blockIdx.x < sum_blocks) {
         const long per = width / 4, total = 2 * a.rows * per;
         const long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
@@ -963,26 +970,25 @@ cudaError_t bwd_typed(const BwdDev& d, const Plan& p, cudaStream_t st) {
         if constexpr (tc) {
             e = launch_states_tc(d, write, write && p.whole, st);
         } else if (write) {
-            scan_states_kernel<IO, N, true><<<grid, kScanThreads, SL::bytes, st>>>(d, p.whole);
+            launch_next(scan_states_kernel<IO, N, true>, grid, kScanThreads, SL::bytes, st, d, p.whole);
         } else {
-            scan_states_kernel<IO, N, false><<<grid, kScanThreads, SL::bytes, st>>>(d, false);
+            launch_next(scan_states_kernel<IO, N, false>, grid, kScanThreads, SL::bytes, st, d, false);
         }
     };
     if (!p.whole) {
         states(false);
         if (e != cudaSuccess) return e;
         constexpr int elems = kScanP * N;
-        scan_states_join_kernel<<<dim3(static_cast<unsigned>(p.seg.B) * d.H, (elems / 4 + 255) / 256, 2), 256, 0,
-                                  st>>>(d, elems);
+        launch_next(scan_states_join_kernel, dim3(static_cast<unsigned>(p.seg.B) * d.H, (elems / 4 + 255) / 256, 2), 256, 0,
+                    st, d, elems);
     }
     states(true);
     if (e != cudaSuccess) return e;
-    scan_grad_kernel<IO, N>
-        <<<static_cast<unsigned>(p.chunk_count * d.G * d.shares), kScanThreads, GL::bytes, st>>>(d);
+    launch_next(scan_grad_kernel<IO, N>, static_cast<unsigned>(p.chunk_count * d.G * d.shares), kScanThreads, GL::bytes, st, d);
     const int width = d.G * N;
     const unsigned sum_blocks =
         d.shares > 1 ? static_cast<unsigned>((2 * p.rows * (width / 4) + 255) / 256) : 0;
-    scan_sum_kernel<IO><<<sum_blocks + d.H, 256, 0, st>>>(d, width, sum_blocks);
+    launch_next(scan_sum_kernel<IO>, sum_blocks + d.H, 256, 0, st, d, width, sum_blocks);
     return cudaGetLastError();
 }
 

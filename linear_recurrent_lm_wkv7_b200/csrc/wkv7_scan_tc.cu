@@ -209,6 +209,10 @@ __device__ __forceinline__ void chunk_decays128(Decays128& d, const float (&dt)[
 template <bool OUT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     scan_tc_kernel(const TcArgs a, bool whole, const __grid_constant__ TcMaps maps) {
+    if constexpr (OUT)
+        chain_wait();
+    else
+        chain_next();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
@@ -717,6 +721,8 @@ struct StMaps {
 template <bool WRITE>
 __global__ void __launch_bounds__(kStThreads, 1)
     states_tc_kernel(const BwdDev a, bool whole, const __grid_constant__ StMaps maps) {
+    chain_wait();
+    chain_next();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
@@ -997,7 +1003,11 @@ cudaError_t launch_scan_tc(const ScanArgs& p, const SegMap& map, bool whole, boo
     cudaError_t e;
     if (out) {
         e = configure_smem_once(scan_tc_kernel<true>, kTcSmem, cfg_out);
-        if (e == cudaSuccess) scan_tc_kernel<true><<<grid, kTcThreads, kTcSmem, stream>>>(a, whole, maps);
+        if (e != cudaSuccess) return e;
+        if (whole)
+            scan_tc_kernel<true><<<grid, kTcThreads, kTcSmem, stream>>>(a, whole, maps);
+        else
+            e = launch_next(scan_tc_kernel<true>, grid, kTcThreads, kTcSmem, stream, a, whole, maps);
     } else {
         e = configure_smem_once(scan_tc_kernel<false>, kTcSmem, cfg_state);
         if (e == cudaSuccess) scan_tc_kernel<false><<<grid, kTcThreads, kTcSmem, stream>>>(a, whole, maps);
@@ -1017,10 +1027,10 @@ cudaError_t launch_states_tc(const BwdDev& d, bool write, bool whole, cudaStream
     cudaError_t e;
     if (write) {
         e = configure_smem_once(states_tc_kernel<true>, kStSmem, cfg_w);
-        if (e == cudaSuccess) states_tc_kernel<true><<<grid, kStThreads, kStSmem, stream>>>(d, whole, maps);
+        if (e == cudaSuccess) launch_next(states_tc_kernel<true>, grid, kStThreads, kStSmem, stream, d, whole, maps);
     } else {
         e = configure_smem_once(states_tc_kernel<false>, kStSmem, cfg_s);
-        if (e == cudaSuccess) states_tc_kernel<false><<<grid, kStThreads, kStSmem, stream>>>(d, whole, maps);
+        if (e == cudaSuccess) launch_next(states_tc_kernel<false>, grid, kStThreads, kStSmem, stream, d, whole, maps);
     }
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
