@@ -107,9 +107,10 @@ __device__ __forceinline__ float act_grad_f32(float x, int act) {
 // ---------------------------------------------------------------- launches of one call
 // A call's second and later kernels are launched while the one before still runs, so that
 // the way to their start is over when it ends.  Each begins with chain_wait, for every
-// thread of every block: it returns when the kernel before has completed (and with it all
-// before that one).  chain_next, in the kernel before, lets the next one come.  A call's first
-// kernel is launched plainly, and so starts when all that the stream holds has ended.
+// thread of every block that reads or overwrites what came before: it returns when the
+// kernel before has completed (and with it all before that one).  chain_next, in the kernel
+// before, lets the next one come.  A call's first kernel is launched plainly, and so starts
+// when all that the stream holds has ended.
 // (Four kernels of a packed fp32 scan, 5003 rows of H12 N64: 88 us in plain launches, 82 so.)
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

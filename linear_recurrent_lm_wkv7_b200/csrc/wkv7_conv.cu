@@ -13,7 +13,7 @@
 // Measured: packed fp32 [16384][2307] W3 (a row stride that no vector divides, so accesses
 // of one element) 58.9 us, 5.1 TB/s; bf16 B4 T1024 C2304 W4 13.1 us, 2.9 TB/s, the tail of
 // a launch that short; a token of 256 sequences (C2816 W4) 6.7 us; gradients of B4 T1024
-// C2304 W4 23.7 us + 2.6 for the sums, where issue slots (activation, its derivative, four
+// C2304 W4 23.7 us with the sums, where issue slots (activation, its derivative, four
 // windows) weigh as much as memory.
 #include "seq_common.cuh"
 
@@ -218,8 +218,9 @@ __global__ void __launch_bounds__(kThreads)
 //   dw[j] = sum_t g_t x_{t-W+1+j},   dbias = sum_t g_t
 // and the rows of s0 get the same sum as dx at the positions before the sequence.
 // A block covers 32 vectors of channels and 8 strips; its sums of dw and dbias over
-// the strips go to the workspace, [block][(W + 1)][C], and conv_bwd_sum_kernel adds
-// the blocks in their order, so the result does not depend on timing.
+// the strips go to the workspace, [block][(W + 1)][C], and conv_bwd_tail_kernel adds
+// the blocks in their order, so the result does not depend on timing.  ds0 is made there too (as
+// blocks of the first launch it lasted 2.4 us longer, behind a full wave of strips).
 constexpr int kLanes = 32, kStrips = kThreads / kLanes;
 constexpr int kAheadB = 4;
 constexpr int kVecB = 4;  // channels per thread: x, g, w and dw windows of W rows stay in registers
@@ -273,21 +274,14 @@ template <typename IO, int VEC, int W>
 __global__ void __launch_bounds__(kThreads, 2)
     conv_bwd_kernel(const IO* __restrict__ x, long ldx, const float* __restrict__ w, const float* __restrict__ bias,
                     const IO* __restrict__ s0, const IO* __restrict__ dy, long lddy, const IO* __restrict__ dsT,
-                    IO* __restrict__ dx, long lddx, IO* __restrict__ ds0, float* __restrict__ part,
-                    const int32_t* __restrict__ offs, int B, int T, long rows, int C, int act, int strip_rows,
-                    unsigned row_blocks, int* status) {
+                    IO* __restrict__ dx, long lddx, float* __restrict__ part, const int32_t* __restrict__ offs, int B,
+                    int T, long rows, int C, int act, int strip_rows, int* status) {
     chain_next();
     const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
     const int c = (blockIdx.y * kLanes + lane) * VEC;
     const bool live = c < C;
     float wr[W][VEC], br[VEC];
     if (live) load_filter<VEC, W>(wr, br, w, bias, c);
-    if (blockIdx.x >= row_blocks) {  // ds0: one sequence per strip slot
-        const long n = static_cast<long>(blockIdx.x - row_blocks) * kStrips + sub;
-        if (live && n < B)
-            write_state_grad<IO, VEC, W>(x, ldx, s0, dy, lddy, dsT, ds0, wr, br, offs, T, C, act, n, c, status);
-        return;
-    }
     float acc[W + 1][VEC];  // dw, then dbias
 #pragma unroll
     for (int j = 0; j <= W; ++j)
@@ -416,10 +410,26 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // dw [C][W] and dbias [C] from the blocks' sums: 32 columns of [(W + 1)][C] per
-// block, 8 threads each adding every eighth partial, then the eight in order.
+// block, 8 threads each adding every eighth partial, then the eight in order.  The blocks from
+// sum_blocks on: ds0, one thread per (sequence, vector of channels), from nothing that the
+// kernel before writes.
+template <typename IO, int VEC, int W>
 __global__ void __launch_bounds__(kThreads)
-    conv_bwd_sum_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ dbias, long nblk,
-                        int C, int W) {
+    conv_bwd_tail_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ dbias, long nblk,
+                         int C, unsigned sum_blocks, const IO* __restrict__ x, long ldx, const float* __restrict__ w,
+                         const float* __restrict__ bias, const IO* __restrict__ s0, const IO* __restrict__ dy,
+                         long lddy, const IO* __restrict__ dsT, IO* __restrict__ ds0,
+                         const int32_t* __restrict__ offs, int B, int T, int act, int* status) {
+    if (blockIdx.x >= sum_blocks) {
+        const int Cv = C / VEC;
+        const long i = static_cast<long>(blockIdx.x - sum_blocks) * kThreads + threadIdx.x;
+        if (i >= static_cast<long>(B) * Cv) return;
+        const int c = static_cast<int>(i % Cv) * VEC;
+        float wr[W][VEC], br[VEC];
+        load_filter<VEC, W>(wr, br, w, bias, c);
+        write_state_grad<IO, VEC, W>(x, ldx, s0, dy, lddy, dsT, ds0, wr, br, offs, T, C, act, i / Cv, c, status);
+        return;
+    }
     chain_wait();
     __shared__ float red[kStrips][kLanes];
     const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
@@ -487,17 +497,24 @@ template <typename IO, int VEC, int W>
 cudaError_t bwd_typed(const ConvBwdArgs& p, cudaStream_t st) {
     const long rows = p.seq_offsets ? p.T : static_cast<long>(p.B) * p.T;
     const long nblk = conv_bwd_blocks(rows);
-    const unsigned ns = p.ds0 ? static_cast<unsigned>((p.B + kStrips - 1) / kStrips) : 0;
-    const dim3 grid(static_cast<unsigned>(nblk) + ns, (p.C / VEC + kLanes - 1) / kLanes);
-    if (grid.x)
-        conv_bwd_kernel<IO, VEC, W><<<grid, kThreads, 0, st>>>(
-            static_cast<const IO*>(p.x), p.ldx, p.w, p.bias, static_cast<const IO*>(p.s0),
-            static_cast<const IO*>(p.dy), p.lddy, static_cast<const IO*>(p.dsT), static_cast<IO*>(p.dx), p.lddx,
-            static_cast<IO*>(p.ds0), p.ws, p.seq_offsets, p.B, p.T, rows, p.C, p.act, kBwdStripRows,
-            static_cast<unsigned>(nblk), p.status);
-    const long cols = static_cast<long>(W + 1) * p.C;
-    launch_next(conv_bwd_sum_kernel, static_cast<unsigned>((cols + kLanes - 1) / kLanes), kThreads, 0, st, p.ws, p.dw,
-                p.dbias, nblk, p.C, W);
+    const IO *x = static_cast<const IO*>(p.x), *dy = static_cast<const IO*>(p.dy), *s0 = static_cast<const IO*>(p.s0),
+             *dsT = static_cast<const IO*>(p.dsT);
+    const int Cv = p.C / VEC;
+    const unsigned sums = static_cast<unsigned>((static_cast<long>(W + 1) * p.C + kLanes - 1) / kLanes);
+    const unsigned states = p.ds0 ? static_cast<unsigned>((static_cast<long>(p.B) * Cv + kThreads - 1) / kThreads) : 0;
+    auto* tail = conv_bwd_tail_kernel<IO, VEC, W>;
+    if (nblk == 0) {  // the call's only kernel: not to start before what the stream holds has ended
+        tail<<<sums + states, kThreads, 0, st>>>(p.ws, p.dw, p.dbias, nblk, p.C, sums, x, p.ldx, p.w, p.bias, s0, dy,
+                                                 p.lddy, dsT, static_cast<IO*>(p.ds0), p.seq_offsets, p.B, p.T, p.act,
+                                                 p.status);
+        return cudaGetLastError();
+    }
+    const dim3 grid(static_cast<unsigned>(nblk), (Cv + kLanes - 1) / kLanes);
+    conv_bwd_kernel<IO, VEC, W><<<grid, kThreads, 0, st>>>(x, p.ldx, p.w, p.bias, s0, dy, p.lddy, dsT,
+                                                           static_cast<IO*>(p.dx), p.lddx, p.ws, p.seq_offsets, p.B,
+                                                           p.T, rows, p.C, p.act, kBwdStripRows, p.status);
+    launch_next(tail, sums + states, kThreads, 0, st, p.ws, p.dw, p.dbias, nblk, p.C, sums, x, p.ldx, p.w, p.bias, s0, dy,
+                p.lddy, dsT, static_cast<IO*>(p.ds0), p.seq_offsets, p.B, p.T, p.act, p.status);
     return cudaGetLastError();
 }
 
