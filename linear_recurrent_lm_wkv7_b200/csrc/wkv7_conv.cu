@@ -13,7 +13,7 @@
 // Measured: packed fp32 [16384][2307] W3 (a row stride that no vector divides, so accesses
 // of one element) 58.9 us, 5.1 TB/s; bf16 B4 T1024 C2304 W4 13.1 us, 2.9 TB/s, the tail of
 // a launch that short; a token of 256 sequences (C2816 W4) 6.7 us; gradients of B4 T1024
-// C2304 W4 23.7 us with the sums, where issue slots (activation, its derivative, four
+// C2304 W4 25.5 us with the sums and ds0, where issue slots (activation, its derivative, four
 // windows) weigh as much as memory.
 #include "seq_common.cuh"
 

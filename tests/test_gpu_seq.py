@@ -604,6 +604,35 @@ def test_graph_and_streams(wk):
     assert torch.equal(y, want[0][0][0]) and torch.equal(sT, want[0][0][1])
 
 
+@pytest.mark.parametrize("io,N", [("bf16", 128), ("f32", 64)])
+def test_calls_at_once(wk, io, N):
+    """Calls of several kernels each, in turn on two streams and behind one another: every
+    one gives the bits of a call alone."""
+    ins = [{k: cuda(v) for k, v in scan_inputs((1, 1500), 1, 2, N, 1, io, seed=s).items()} for s in (1, 2)]
+
+    def run(v, stream=None):
+        kw = dict(D=v["D"], dt_bias=v["dt_bias"], s0=v["s0"], stream=stream)
+        y = wk.selective_scan(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], **kw)
+        g = wk.selective_scan_backward(v["x"], v["dt"], v["A"], v["Bm"], v["Cm"], v["dy"], dsT=v["dsT"], **kw)
+        rows = v["x"].reshape(1, 1500, -1)
+        z = wk.causal_conv(rows, v["w"], act="silu", stream=stream)
+        h = wk.causal_conv_backward(rows, v["w"], rows, act="silu", stream=stream)
+        n = wk.group_norm(rows, 2, act="silu", stream=stream)
+        return [t for o in (y, g, z, h, n) for t in o if t is not None]
+
+    for s, v in enumerate(ins):
+        v["w"] = torch.randn(128, 4, generator=torch.Generator().manual_seed(s)).cuda()
+    want = [run(v) for v in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    got = [[run(v, st) for v, st in zip(ins, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for a, b in zip(turn, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert wk.wkv7_get_device_status() == 0
+
+
 def test_empty_calls(wk):
     """No tokens: states pass on, gradients of parameters are zero."""
     s0 = torch.randn(2, 3, 24, device="cuda")
