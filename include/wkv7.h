@@ -323,7 +323,7 @@ int wkv7_backward_noalloc(const void* r, const void* w_log, const void* k, const
  * State-space layers: a short causal convolution, a selective scan (the sibling of
  * the WKV recurrence with one decay per head and token and no removal term) and the
  * group norm that reads out either recurrence.  "RWKV-7 Goose architecture analysis"
- * sets the WKV state beside such scans (its comparison of RWKV, Mamba and RetNet); it
+ * sets the WKV state beside such scans (its comparison of recurrent architectures); it
  * prints no listing of them, so the formulas here are the operators' definitions.
  *
  * Differences from the conventions above, for these entry points only
