@@ -199,6 +199,16 @@ def test_scan_packed(wk, io):
     check_scan(wk, inp, offsets(lens), longest=129)
 
 
+@pytest.mark.parametrize("io,dt,N", [("f32", "bf16", 32), ("bf16", "f32", 32), ("bf16", "f32", 128)])
+def test_scan_dt_of_another_type(wk, io, dt, N):
+    """dt (and its gradient) in a type of its own, dense and packed."""
+    lens = [100, 0, 150]
+    for lead, B, offs in (((2, 130), 2, None), ((sum(lens),), 3, offsets(lens))):
+        inp = scan_inputs(lead, B, 4, N, 2, io, seed=21)
+        inp["dt"] = inp["dt"].to(DT[dt])
+        check_scan(wk, inp, offs, longest=150)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_scan_segments(wk, io):
     """Few heads and a long sequence: cut into segments, forwards and backwards, dense
@@ -631,6 +641,33 @@ def test_calls_at_once(wk, io, N):
         for a, b in zip(turn, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert wk.wkv7_get_device_status() == 0
+
+
+@pytest.mark.parametrize("N", [32, 128])
+def test_offsets_past_32_bits(wk, N):
+    """Rows so far apart that the last lie more than 2^31 elements behind the first."""
+    T, H, ld = 600, 2, 1 << 22
+    d = {k: cuda(v) for k, v in scan_inputs((T,), 1, H, N, 1, "bf16", seed=3).items()}
+    buf = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda")
+    assert (T - 1) * ld > 1 << 31
+    far = buf.as_strided((T, H, 64), (ld, 64, 1))
+    far.copy_(d["x"])
+    offs = offsets([T]).cuda()
+    w = torch.randn(128, 4, generator=torch.Generator().manual_seed(1)).cuda()
+    outs = []
+    for x in (d["x"], far):
+        rows = x.view(T, 128) if x is not far else buf.as_strided((T, 128), (ld, 1))
+        kw = dict(s0=d["s0"][:1], seq_offsets=offs)
+        out = list(wk.selective_scan(x, d["dt"], d["A"], d["Bm"], d["Cm"], **kw))
+        out += wk.selective_scan_backward(x, d["dt"], d["A"], d["Bm"], d["Cm"], x, dsT=d["dsT"][:1], **kw)
+        out += wk.causal_conv(rows, w, seq_offsets=offs, act="silu")
+        out += wk.causal_conv_backward(rows, w, rows, seq_offsets=offs, act="silu")
+        y, stats = wk.group_norm(rows, H, act="silu", want_stats=True)
+        out += (y, stats, *wk.group_norm_backward(rows, H, stats, rows, act="silu"))
+        outs.append([t.clone() for t in out if t is not None])
+    assert wk.wkv7_get_device_status() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
 
 
 def test_empty_calls(wk):
