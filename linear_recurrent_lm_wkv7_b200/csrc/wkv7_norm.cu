@@ -567,6 +567,13 @@ Split split_of(long N, long L, int C, int vec) {
     return s;
 }
 
+// Floats of the forward's partial moments, three to a (sample, group, tile, split).  The
+// statistics that no caller wants lie behind them and are stored in pairs: rounded up, so
+// that they begin on 16 bytes.
+size_t moment_floats(const Split& s, long N, int G) {
+    return (static_cast<size_t>(N) * s.splits * s.tiles * G * 3 + 3) / 4 * 4;
+}
+
 // The row form's team: the smallest that holds nv vectors, 0 when none does.
 // Up to 32 lanes hold one vector each, one warp 2 or 4, a block 1 to 4.
 int team_of(int nv) {
@@ -635,7 +642,7 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
     }
     const Split s = split_of(p.N, p.L, p.C, VEC);
     float* part = p.ws;
-    float* stats = p.stats ? p.stats : part + static_cast<size_t>(p.N) * s.splits * s.tiles * p.G * 3;
+    float* stats = p.stats ? p.stats : part + moment_floats(s, p.N, p.G);
     const dim3 grid(static_cast<unsigned>(p.N) * s.splits, s.tiles);
     norm_stats_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, part, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows);
     // A launch less where the blocks can join the moments on the side: up to kJoinMost of
@@ -706,7 +713,7 @@ size_t ws_floats(int N, int L, int C, int G, bool backward) {
         } else {
             const Split s = split_of(N, L, C, vec);
             n = backward ? static_cast<size_t>(N) * s.splits * 2 * C + static_cast<size_t>(N) * G * 2
-                         : static_cast<size_t>(N) * s.splits * s.tiles * G * 3 + static_cast<size_t>(N) * G * 2;
+                         : moment_floats(s, N, G) + static_cast<size_t>(N) * G * 2;
         }
         most = n > most ? n : most;
     }

@@ -456,6 +456,21 @@ def test_norm_over_tokens(wk, io, N, L, C, groups):
     check_norm(wk, (N, L, C), groups, io, None, affine=False, seed=L + 1)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("N,L,C,groups", [(1, 16384, 960, 15), (1, 16000, 960, 15), (1, 5000, 960, 15),
+                                          (1, 16384, 255, 15), (1, 12000, 255, 255), (3, 9001, 240, 240)])
+def test_norm_joined_by_a_launch(wk, io, N, L, C, groups):
+    """Few samples of many rows and groups: more moments than the blocks that write y join on
+    the side, so a launch of its own joins them.  (Blocks' moments: splits x (groups of a tile
+    + 1) x (tiles of a group + 1), above 8192 in fp32 for all of these.)  With and without
+    statistics of the caller's, and the gradient."""
+    check_norm(wk, (N, L, C), groups, io, "silu", seed=L + C)
+    x = (torch.randn(N, L, C, generator=torch.Generator().manual_seed(C)) + 0.5).to(DT[io]).cuda()
+    y, stats = wk.group_norm(x, groups, want_stats=True)
+    assert torch.equal(wk.group_norm(x, groups), y) and torch.isfinite(stats).all()
+    assert wk.wkv7_get_device_status() == 0
+
+
 @pytest.mark.parametrize("shape", [(9, 128), (2, 50, 128)])
 def test_norm_far_from_zero(wk, shape):
     """A mean of a thousand deviations: the squares are taken about the mean."""

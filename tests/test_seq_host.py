@@ -156,6 +156,20 @@ def test_norm_refusals(wk):
     assert back(wsb=need, db=ok["dw"]) == -1 and back(G=7) == -1
 
 
+@pytest.mark.parametrize("io,vec", [(0, 4), (1, 8)])
+def test_norm_workspace_keeps_statistics_aligned(wk, io, vec):
+    """The split form without statistics of the caller's keeps them, pairs of floats, at the
+    end of the workspace: they begin on 16 bytes whatever the number of partial moments."""
+    query = wk.wkv7_group_norm_workspace_bytes
+    shapes = [(1, L, 960, 15) for L in (4104, 5000, 8192, 16000, 16384)]
+    shapes += [(1, 16384, 480, 15), (1, 16384, 255, 15), (1, 16384, 255, 255), (3, 5001, 33, 11), (1, 1, 10007, 1)]
+    shapes += [(N, L, Cg * G, G) for N in (1, 3, 7) for L in (2, 999, 4097, 11111) for G in (1, 3, 15, 41)
+               for Cg in (1, 5, vec, 7 * vec, 64)]
+    for N, L, C, G in shapes:
+        n = query(N, L, C, G, io)
+        assert n > 0 and (n - 8 * N * G) % 16 == 0, (N, L, C, G)
+
+
 def test_python_refusals(wk):
     x = torch.zeros(2, 8, 16)
     w = torch.zeros(16, 4)
