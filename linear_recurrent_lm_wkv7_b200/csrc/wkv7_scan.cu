@@ -252,16 +252,14 @@ __global__ void __launch_bounds__(kScanThreads, FwdLayout<IO, N>::resident)
                 }
             }
         }
-        // ---- S <- exp(l_64) S + (X^T delta exp(l_64 - l)) B
-        {
-            const float tot = d.total;
-            run *= tot;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[i][e] *= tot;
-        }
+        // ---- S <- exp(l_64) S + (X^T delta exp(l_64 - l)) B, the product from zero: the tensor cores
+        // cut their sums, and a state that was their accumulator lost 2^-23 at every step (1.4e-4
+        // of it after 8192 tokens of fp32, 2e-4 of bf16, where little decays)
+        run *= d.total;
         if (has_n) {
+            float add[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) add[i][0] = add[i][1] = add[i][2] = add[i][3] = 0.f;
 #pragma unroll
             for (int k = 0; k < kChunk; k += 16) {
                 uint32_t fx[PI][4], fa[kStatePlanes][4];
@@ -275,10 +273,15 @@ __global__ void __launch_bounds__(kScanThreads, FwdLayout<IO, N>::resident)
                 for (int i = 0; i < NT; i += 2) {
                     uint32_t fb[2][PI][2];
                     frag_b_t<TB>(fb, sB, n0 + i * 8, k, lane);
-                    mma_planes<kStatePlanes, PI>(S[i], fa, fb[0]);
-                    mma_planes<kStatePlanes, PI>(S[i + 1], fa, fb[1]);
+                    mma_planes<kStatePlanes, PI>(add[i], fa, fb[0]);
+                    mma_planes<kStatePlanes, PI>(add[i + 1], fa, fb[1]);
                 }
             }
+            const float tot = d.total;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[i][e] = fmaf(tot, S[i][e], add[i][e]);
         }
         if constexpr (OUT) {
             __syncthreads();  // M is complete

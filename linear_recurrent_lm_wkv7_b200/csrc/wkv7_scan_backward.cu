@@ -54,7 +54,7 @@ struct StateLayout {
 // backwards.  WRITE: start from the true state and write it at every chunk; otherwise
 // from zero, and only the segment's end and decay are wanted.
 template <typename IO, int N, bool WRITE>
-__global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 || N <= 64 ? 2 : 1)
     scan_states_kernel(const BwdDev a, bool whole) {
     chain_wait();
     chain_next();
@@ -181,15 +181,11 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
                 }
             }
         }
-        {
-            const float tot = d.total;
-            run *= tot;
+        run *= d.total;
+        if (has_n) {  // the product from zero, as in scan_kernel (wkv7_scan.cu)
+            float add[NT][4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[j][e] *= tot;
-        }
-        if (has_n) {
+            for (int j = 0; j < NT; ++j) add[j][0] = add[j][1] = add[j][2] = add[j][3] = 0.f;
             const uint32_t sx = stage(i), sB = sx + TX::bytes;
 #pragma unroll
             for (int k = 0; k < kChunk; k += 16) {
@@ -212,10 +208,15 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 ? 2 : 1)
                 for (int j = 0; j < NT; j += 2) {
                     uint32_t fb[2][PI][2];
                     frag_b_t<TB>(fb, sB, n0 + j * 8, k, lane);
-                    mma_planes<PC, PI>(S[j], fa, fb[0]);
-                    mma_planes<PC, PI>(S[j + 1], fa, fb[1]);
+                    mma_planes<PC, PI>(add[j], fa, fb[0]);
+                    mma_planes<PC, PI>(add[j + 1], fa, fb[1]);
                 }
             }
+            const float tot = d.total;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[j][e] = fmaf(tot, S[j][e], add[j][e]);
         }
     }
     float* dst = nullptr;

@@ -271,6 +271,50 @@ def test_scan_many_sequences(wk):
         check_scan(wk, inp, offsets(lens), longest=3)
 
 
+@pytest.mark.parametrize("io,N", [("f32", 16), ("f32", 64), ("f32", 128), ("bf16", 16), ("bf16", 64), ("bf16", 128)])
+def test_scan_long_sequences_keep_their_sums(wk, io, N):
+    """Sequences of 8192 tokens that one block each carries from end to end, with decays near
+    one.  All terms are positive, so that nothing cancels and what every step loses shows.
+    Tolerance: K = 128 chunks, each multiplying the state by its decay (ex2: 2^-22) and adding
+    its own sum (a rounding, 2^-24); that sum, from zero, of 4 steps of at most 6 products,
+    each cut once (24 x 2^-23); delta 2^-20.  The tcgen05 kernels' chunks of 128 have 8 steps
+    of 3.  dA is a sum of products of two states: twice that, and the sum over rows."""
+    B, T, H = 4, 8192, 32
+    g = torch.Generator(device="cuda").manual_seed(N)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").abs().to(DT[io])
+    x, Bm, Cm, dy = r(B, T, H, 64), r(B, T, 1, N), r(B, T, 1, N), r(B, T, H, 64)
+    dt, A = r(B, T, H), -0.5 - torch.rand(H, generator=g, device="cuda")
+    bias = torch.full((H,), -10.0, device="cuda")  # a decay of some e^-1 over the sequence
+    s0, dsT = r(B, H, 64, N).float(), r(B, H, 64, N).float()
+    # no segments: the workspace holds the chunks' decays alone
+    assert wk.wkv7_selective_scan_workspace_bytes(B, T, H, 64, N, False) == B * T // 64 * H * 324 * 4
+    kw = dict(dt_bias=bias, s0=s0)
+    _, sT = wk.selective_scan(x, dt, A, Bm, Cm, **kw)
+    grads = wk.selective_scan_backward(x, dt, A, Bm, Cm, dy, dsT=dsT, **kw)
+    assert wk.wkv7_get_device_status() == 0
+
+    delta = torch.nn.functional.softplus(dt.double() + bias.double())
+    a = torch.exp(delta * A.double())
+    keep = N == 16  # dA: 8.6 GB of states
+    S, states = s0.double(), []
+    for t in range(T):
+        if keep:
+            states.append(S)
+        S = a[:, t, :, None, None] * S
+        S += (delta[:, t, :, None] * x[:, t].double())[..., None] * Bm[:, t, :, None].double()
+    dS, dA = dsT.double(), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for t in range(T - 1, -1, -1):
+        dS = dS + dy[:, t].double()[..., None] * Cm[:, t, :, None].double()
+        if keep:
+            dA += ((dS * states.pop()).sum((2, 3)) * a[:, t] * delta[:, t]).sum(0)
+        dS = a[:, t, :, None, None] * dS
+    e = T // 64 * (2.0 ** -24 + 2.0 ** -22) + 24 * 2.0 ** -23 + 2.0 ** -20
+    close("sT", sT, S.cpu(), S.cpu(), e)
+    close("ds0", grads[7], dS.cpu(), dS.cpu(), e)
+    if keep:
+        close("dA", grads[2], dA.cpu(), dA.abs().cpu(), 2 * e + B * T * 2.0 ** -24)
+
+
 def test_calls_on_two_streams(wk):
     """The same kernels from two streams at once."""
     ins = []
