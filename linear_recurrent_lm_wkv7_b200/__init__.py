@@ -341,12 +341,11 @@ def causal_conv_step(x, w, state, bias=None, act=None, y=None, stream=None):
     """One token per sequence of ``causal_conv``: ``x`` [B, C], ``state`` [B, W-1, C]
     updated in place.  Returns y ([B, C])."""
     C, W = w.shape
-    if y is None:
-        if stream is None:
-            y = _new(x)
-        else:
-            with _outputs(x, stream, (x, w, state, bias)):
-                y = _new(x)
+    if stream is not None:
+        with _outputs(x, stream, (x, w, state, bias, y)):
+            y = _new(x) if y is None else y
+    elif y is None:
+        y = _new(x)
     wkv7_causal_conv_step(x, w, bias, state, y, state, x.shape[0], C, W, act, stream)
     return y
 
@@ -396,12 +395,11 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, dt_softpl
     ([B, H, 64])."""
     B, H, P = x.shape
     _, G, N = Bm.shape
-    if y is None:
-        if stream is None:
-            y = _new(x)
-        else:
-            with _outputs(x, stream, (x, dt, A, Bm, Cm, state, D, dt_bias)):
-                y = _new(x)
+    if stream is not None:
+        with _outputs(x, stream, (x, dt, A, Bm, Cm, state, D, dt_bias, y)):
+            y = _new(x) if y is None else y
+    elif y is None:
+        y = _new(x)
     wkv7_selective_scan_step(x, dt, A, Bm, Cm, D, dt_bias, state, y, state, B, H, P, N, G, dt_softplus, stream)
     return y
 

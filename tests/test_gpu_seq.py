@@ -673,6 +673,37 @@ def test_graph_and_streams(wk):
     assert torch.equal(y, want[0][0][0]) and torch.equal(sT, want[0][0][1])
 
 
+def test_steps_on_a_stream_keep_freed_inputs(wk):
+    """An input that is freed behind a step on a busy stream is not handed out again before
+    that stream is done with it, with y allocated and with y given."""
+    side = torch.cuda.Stream()
+    w, A = torch.randn(256, 4, device="cuda"), -torch.ones(4, device="cuda")
+    x0, c0 = torch.randn(64, 256, device="cuda"), torch.randn(64, 3, 256, device="cuda")
+    dt, b, s0 = (torch.randn(64, *s, device="cuda") for s in ((4,), (1, 16), (4, 64, 16)))
+
+    def conv(x, st, y, stream):
+        return wk.causal_conv_step(x, w, st, act="silu", y=y, stream=stream)
+
+    def scan(x, st, y, stream):
+        return wk.selective_scan_step(x.view(64, 4, 64), dt, A, b, b, st, y=None if y is None else y.view(64, 4, 64),
+                                      stream=stream).view(64, 256)
+
+    for call, state in ((conv, c0), (scan, s0)):
+        want = call(x0, state.clone(), None, None)
+        for given in (False, True):
+            x, st, y = x0.clone(), state.clone(), torch.empty_like(x0) if given else None
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            got = call(x, st, y, side)
+            at = x.data_ptr()
+            del x
+            new = torch.full_like(x0, float("nan"))
+            assert new.data_ptr() != at
+            side.synchronize()
+            assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("io,N", [("bf16", 128), ("f32", 64)])
 def test_calls_at_once(wk, io, N):
     """Calls of several kernels each, in turn on two streams and behind one another: every

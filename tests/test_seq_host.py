@@ -195,6 +195,27 @@ def test_python_refusals(wk):
         ld(torch.zeros(2, 8, 4, 80)[..., :64], 2, 256, "x")
 
 
+def test_steps_mark_every_tensor_for_another_stream(wk, monkeypatch):
+    """A step on a stream that is given marks its inputs, the state and y as used there, also
+    where y is the caller's."""
+    marked = []
+    monkeypatch.setattr(wk, "_outputs", lambda like, stream, inputs: marked.append((stream, inputs)) or wk._NO_STREAM)
+    monkeypatch.setattr(wk, "wkv7_causal_conv_step", lambda *a: None)
+    monkeypatch.setattr(wk, "wkv7_selective_scan_step", lambda *a: None)
+    x, w, st, b, y = torch.zeros(2, 8), torch.zeros(8, 4), torch.zeros(2, 3, 8), torch.zeros(8), torch.zeros(2, 8)
+    u, dt, A, B, S = torch.zeros(2, 4, 64), torch.zeros(2, 4), torch.zeros(4), torch.zeros(2, 1, 16), torch.zeros(2, 4, 64, 16)
+    v = torch.zeros(2, 4, 64)
+    for out, mine in ((y, [x, w, st, b, y]), (None, [x, w, st, b])):
+        wk.causal_conv_step(x, w, st, bias=b, y=out, stream=7)
+        stream, seen = marked.pop()
+        assert stream == 7 and all(any(t is s for s in seen) for t in mine)
+    for out, mine in ((v, [u, dt, A, B, S, v]), (None, [u, dt, A, B, S])):
+        wk.selective_scan_step(u, dt, A, B, B, S, D=A, dt_bias=A, y=out, stream=7)
+        stream, seen = marked.pop()
+        assert stream == 7 and all(any(t is s for s in seen) for t in mine)
+    assert wk.causal_conv_step(x, w, st, y=y) is y and not marked
+
+
 # ---------------------------------------------------------------- the references themselves
 def test_reference_scan_gradients():
     """The explicit gradients against autograd of the same recurrence."""
