@@ -37,17 +37,18 @@ bool overlap(const Span& a, const Span& b) {
     return true;
 }
 
-// Outputs against every input and against each other; an input at the same place as
-// the output named `inplace` (and of its extent) is let through.
-bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins, const void* inplace = nullptr) {
+// Outputs against every input and against each other.
+bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
     for (auto o = outs.begin(); o != outs.end(); ++o) {
         for (const Span& i : ins)
-            if (!(inplace && o->p == inplace && i.p == inplace && o->width == i.width) && overlap(*o, i)) return true;
+            if (overlap(*o, i)) return true;
         for (auto q = o + 1; q != outs.end(); ++q)
             if (overlap(*o, *q)) return true;
     }
     return false;
 }
+// A state that may be updated in place, for the list of inputs: none where it is.
+Span state_in(const void* s_in, const void* s_out, int64_t bytes) { return flat(s_in == s_out ? nullptr : s_in, bytes); }
 
 bool misaligned(std::initializer_list<const void*> ptrs) {
     for (const void* p : ptrs)
@@ -110,9 +111,8 @@ int wkv7_causal_conv(const void* x, int64_t ld_x, const float* w, const float* b
     const int64_t st = static_cast<int64_t>(B) * (W - 1) * C * e;
     const int64_t Wc = static_cast<int64_t>(C) * W * 4;
     if (any_overlap({rows_of(y, rows, C, ld_y, e), flat(sT, st)},
-                    {rows_of(x, rows, C, ld_x, e), flat(w, Wc), flat(bias, 4L * C), flat(s0, st),
-                     flat(seq_offsets, 4L * (B + 1))},
-                    sT))
+                    {rows_of(x, rows, C, ld_x, e), flat(w, Wc), flat(bias, 4L * C), state_in(s0, sT, st),
+                     flat(seq_offsets, 4L * (B + 1))}))
         return WKV7_ERR_INVALID_ARG;
     if ((s = wkv7::device_check()) != WKV7_OK) return s;
     if (T == 0 && !sT) return WKV7_OK;
@@ -133,8 +133,7 @@ int wkv7_causal_conv_step(const void* x, int64_t ld_x, const float* w, const flo
     const int64_t st = static_cast<int64_t>(B) * (W - 1) * C * e;
     if (any_overlap({rows_of(y, B, C, ld_y, e), flat(s_out, st)},
                     {rows_of(x, B, C, ld_x, e), flat(w, static_cast<int64_t>(C) * W * 4), flat(bias, 4L * C),
-                     flat(s_in, st)},
-                    s_out))
+                     state_in(s_in, s_out, st)}))
         return WKV7_ERR_INVALID_ARG;
     if ((s = wkv7::device_check()) != WKV7_OK) return s;
     const wkv7::ConvArgs p{x, ld_x, w, bias, s_in, y, ld_y, s_out, B, 1, C, W, nullptr, act, nullptr};
@@ -201,8 +200,7 @@ int wkv7_selective_scan(const void* x, int64_t ld_x, const void* dt, int64_t ld_
     if (any_overlap({rows_of(y, rows, wx, ld_y, e), flat(sT, st), flat(workspace, static_cast<int64_t>(need))},
                     {rows_of(x, rows, wx, ld_x, e), rows_of(dt, rows, H, ld_dt, de), rows_of(Bm, rows, wb, ld_b, e),
                      rows_of(Cm, rows, wb, ld_c, e), flat(A, 4L * H), flat(D_skip, 4L * H), flat(dt_bias, 4L * H),
-                     flat(s0, st), flat(seq_offsets, 4L * (B + 1))},
-                    sT))
+                     state_in(s0, sT, st), flat(seq_offsets, 4L * (B + 1))}))
         return WKV7_ERR_INVALID_ARG;
     if ((s = wkv7::device_check()) != WKV7_OK) return s;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -233,8 +231,7 @@ int wkv7_selective_scan_step(const void* x, int64_t ld_x, const void* dt, int64_
     if (any_overlap({rows_of(y, B, wx, ld_y, e), flat(s_out, st)},
                     {rows_of(x, B, wx, ld_x, e), rows_of(dt, B, H, ld_dt, de), rows_of(Bm, B, wb, ld_b, e),
                      rows_of(Cm, B, wb, ld_c, e), flat(A, 4L * H), flat(D_skip, 4L * H), flat(dt_bias, 4L * H),
-                     flat(s_in, st)},
-                    s_out))
+                     state_in(s_in, s_out, st)}))
         return WKV7_ERR_INVALID_ARG;
     if ((s = wkv7::device_check()) != WKV7_OK) return s;
     const wkv7::ScanArgs p{x, ld_x, dt, ld_dt, A, Bm, ld_b, Cm, ld_c, D_skip, dt_bias, s_in, y, ld_y, s_out,

@@ -64,6 +64,19 @@ def test_conv_refusals(wk, step):
         assert call(y=call.ok["x"] + 64, ldx=128, ldy=128) == -1
 
 
+def test_a_state_in_place_lets_nothing_else_through(wk):
+    """sT may be s0, and no other input even where that starts and ends with it: w, bias or x
+    of the state's extent."""
+    f32 = dict(io=0, C=64)
+    call = conv_call(wk)
+    for k, over in (("w", dict(B=2, W=2)), ("bias", dict(B=1, W=2)), ("x", dict(B=1, W=2, T=1)), ("x", dict(B=1, W=2, T=5))):
+        assert call(**f32, **over, sT=call.ok[k], s0=None) == -1, k
+        assert call(**f32, **over, sT=call.ok[k]) == -1, k
+    step = conv_call(wk, True)
+    for k, over in (("w", dict(B=2, W=2)), ("bias", dict(B=1, W=2)), ("x", dict(B=1, W=2))):
+        assert step(**f32, **over, sT=step.ok[k]) == -1, k
+
+
 def test_conv_backward_refusals(wk):
     lib = wk._lib()
     ok = ptrs("x", "w", "bias", "s0", "dy", "dsT", "dx", "dw", "db", "ds0", "ws") | dict(
