@@ -331,9 +331,10 @@ int wkv7_backward_noalloc(const void* r, const void* w_log, const void* k, const
  *    elements (ld >= width), so that column slices of a projection's output can be
  *    passed without a copy.  Dense batches: row b T + t; packed batches (seq_offsets,
  *    as in wkv7_forward): row t.  Rows of no sequence (before seq_offsets[0] or behind
- *    seq_offsets[B]) are neither read for a result nor written; pairs of offsets that
- *    are not monotone or leave [0, T] count as an empty sequence and set
- *    WKV7_ERR_DEVICE_BOUNDS.
+ *    seq_offsets[B]) are neither read for a result nor written.  A pair of offsets that
+ *    is not monotone or leaves [0, T] counts as an empty sequence (its state passes on)
+ *    and sets WKV7_ERR_DEVICE_BOUNDS; nothing outside the tensors is touched, but the
+ *    rows and states of the other sequences of that call are then unspecified.
  *  - Per-channel and per-head parameters and their gradients are fp32.
  *  - Outputs and workspaces must be disjoint from the inputs and from each other,
  *    except where a state may be updated in place.  Two row sets of one stride may

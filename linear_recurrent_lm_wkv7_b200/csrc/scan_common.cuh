@@ -35,15 +35,18 @@ constexpr int kStatePlanes = 3;
 // How sequences are cut into segments of `seg` tokens (a multiple of 64): dense ones
 // into spb = ceil(T / seg) slots each; packed ones own the slots from
 // offs[n] / seg + n on, which are at least as many as they need and end at
-// T / seg + B at the latest.
+// T / seg + B at the latest.  Where seg covers T, slot n is packed sequence n, whatever the
+// offsets hold: each is looked at, and those of a bad pair pass their states on.
 struct SegMap {
     const int32_t* offs;
     int B, T;
     long seg;
     int spb;
 };
+// Whether slots are found through the offsets.
+inline __host__ __device__ bool seg_cut(const SegMap& m) { return m.offs && m.seg < m.T; }
 inline __host__ __device__ long seg_slots(const SegMap& m) {
-    return m.offs ? m.T / m.seg + m.B : static_cast<long>(m.B) * m.spb;
+    return seg_cut(m) ? m.T / m.seg + m.B : static_cast<long>(m.B) * m.spb;
 }
 // How a kernel that carries one head's state through chunks is best cut (wkv7_scan.cu).
 struct CutCost {
@@ -56,12 +59,12 @@ struct CutCost {
 };
 SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed, const CutCost& cost);
 __device__ __forceinline__ long seg_first(const SegMap& m, int n, long lo) {
-    return m.offs ? lo / m.seg + n : static_cast<long>(n) * m.spb;
+    return seg_cut(m) ? lo / m.seg + n : static_cast<long>(n) * m.spb;
 }
 // Sequence n and rows [r0, r1) of a slot; false when the slot is not in use.
 __device__ __forceinline__ bool seg_rows(const SegMap& m, long slot, int& n, long& r0, long& r1, long& lo, long& hi,
                                          int* status) {
-    if (m.offs) {
+    if (seg_cut(m)) {
         int a = 0, b = m.B - 1;  // the largest n whose first slot is not behind this one
         while (a < b) {
             const int c = (a + b + 1) >> 1;

@@ -119,8 +119,7 @@ __global__ void __launch_bounds__(kScanThreads, FwdLayout<IO, N>::resident)
     long r0, r1, lo, hi;
     const bool used = seg_rows(a.map, slot, n, r0, r1, lo, hi, a.status);
     if (!used) {
-        // an empty sequence passes its state on (its first slot does that)
-        if (!whole || !a.sT || hi > lo || slot != seg_first(a.map, n, lo)) return;
+        if (!whole || !a.sT) return;  // an empty sequence passes its state on
         const long e = (static_cast<long>(n) * a.H + h) * kScanP * N;
         for (int i = tid; i < kScanP * N; i += kScanThreads) a.sT[e + i] = a.s0 ? a.s0[e + i] : 0.f;
         return;
@@ -553,7 +552,7 @@ cudaError_t launch_decays(const DecayArgs& a, cudaStream_t stream) {
 
 SegMap chunk_map(int B, int T, const int32_t* offs) { return SegMap{offs, B, T, kChunk, (T + kChunk - 1) / kChunk}; }
 long chunk_slots(int B, int T, bool packed) {
-    return packed ? T / kChunk + B : static_cast<long>(B) * ((static_cast<long>(T) + kChunk - 1) / kChunk);
+    return packed && T > kChunk ? T / kChunk + B : static_cast<long>(B) * ((static_cast<long>(T) + kChunk - 1) / kChunk);
 }
 
 // The segments' states and decays of either kernel (the size query does not know the io

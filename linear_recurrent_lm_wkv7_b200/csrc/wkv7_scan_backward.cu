@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kScanThreads, sizeof(IO) == 2 || N <= 64 ? 2 :
     int n;
     long r0, r1, lo, hi;
     if (!seg_rows(a.seg, slot, n, r0, r1, lo, hi, a.status)) {
-        if (!whole || !back || !a.ds0 || hi > lo || slot != seg_first(a.seg, n, lo)) return;
+        if (!whole || !back || !a.ds0) return;
         const long e = (static_cast<long>(n) * a.H + h) * kState;  // no tokens: ds0 = dsT
         for (int i = tid; i < kState; i += kScanThreads) a.ds0[e + i] = a.dsT ? a.dsT[e + i] : 0.f;
         return;
@@ -938,7 +938,7 @@ Plan plan_of(int B, int T, int H, int N, int G, int io_dtype, const int32_t* off
                                                         : CutCost{kChunk, 1, 1.0, 1.0, 1.0, 2.0});
     p.whole = p.seg.seg >= T;
     p.chunk = chunk_map(B, T, offs);
-    p.seg_count = packed ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;
+    p.seg_count = packed && !p.whole ? T / p.seg.seg + B : static_cast<long>(B) * p.seg.spb;
     p.chunk_count = chunk_slots(B, T, packed);
     p.rows = packed ? T : static_cast<long>(B) * T;
     p.shares = shares_of(p.chunk_count, G, H / G);

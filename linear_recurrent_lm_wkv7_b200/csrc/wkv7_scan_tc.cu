@@ -232,8 +232,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int n;
     long r0, r1, lo, hi;
     if (!seg_rows(a.map, slot, n, r0, r1, lo, hi, a.status)) {
-        // an empty sequence passes its state on (its first slot does that)
-        if (!whole || !a.sT || hi > lo || slot != seg_first(a.map, n, lo)) return;
+        if (!whole || !a.sT) return;  // an empty sequence passes its state on
         const long e = (static_cast<long>(n) * a.H + h) * kState;
         for (int i = tid; i < kState; i += kTcThreads) a.sT[e + i] = a.s0 ? a.s0[e + i] : 0.f;
         return;
@@ -737,7 +736,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     int n;
     long r0, r1, lo, hi;
     if (!seg_rows(a.seg, slot, n, r0, r1, lo, hi, a.status)) {
-        if (!whole || !back || !a.ds0 || hi > lo || slot != seg_first(a.seg, n, lo)) return;
+        if (!whole || !back || !a.ds0) return;
         const long e = (static_cast<long>(n) * a.H + h) * kState;  // no tokens: ds0 = dsT
         for (int i = tid; i < kState; i += kStThreads) a.ds0[e + i] = a.dsT ? a.dsT[e + i] : 0.f;
         return;

@@ -432,6 +432,26 @@ def test_bad_offsets_are_reported(wk):
     assert wk.wkv7_get_device_status() == -6
 
 
+@pytest.mark.parametrize("io,N", [("f32", 16), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("lens", [(0, 64, 10, 64), (0, 70, 64, 64), (0, -100, -100, 64), (0, 10, 64, 5)])
+def test_bad_offsets_of_whole_sequences(wk, io, N, lens):
+    """Every pair of offsets is looked at, also where sequences are not cut into segments: a bad
+    one is reported, and its sequence's state (and state gradient) passes on."""
+    T, B = 64, 3
+    d = {k: cuda(v) for k, v in scan_inputs((T,), B, 2, N, 1, io, seed=2).items()}
+    offs = torch.tensor(lens, dtype=torch.int32)
+    bad = [n for n in range(B) if not 0 <= offs[n] <= offs[n + 1] <= T]
+    assert bad
+    kw = dict(s0=d["s0"], seq_offsets=offs.cuda())
+    wk.wkv7_get_device_status()
+    _, sT = wk.selective_scan(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], **kw)
+    assert wk.wkv7_get_device_status() == -6
+    ds0 = wk.selective_scan_backward(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["dy"], dsT=d["dsT"], **kw)[7]
+    assert wk.wkv7_get_device_status() == -6
+    for n in bad:
+        assert torch.equal(sT[n], d["s0"][n]) and torch.equal(ds0[n], d["dsT"][n]), n
+
+
 def test_scan_gradient_against_differences(wk):
     """<dy, y> + <dsT, sT> of the kernels along a random direction in every input: central
     differences with step h have a relative error of h^2 and noise of e32 / h; with
