@@ -115,6 +115,13 @@ __device__ void write_state(const IO* x, long ldx, const IO* s0, IO* sT, const i
     for (int i = 0; i < W - 1; ++i) store_vec<VEC>(sT + (n * (W - 1) + i) * C + c, f[i]);
 }
 
+// Where no state is written: a thread per packed sequence looks at its offsets, some of
+// which the rows' blocks pass over when a pair is bad.
+__device__ __forceinline__ void look_at_spans(const int32_t* offs, long n, int B, int T, int* status) {
+    long lo, hi;
+    if (n < B) seq_span(offs, static_cast<int>(n), T, lo, hi, status);
+}
+
 // Blocks [0, blocks_rows): y, one thread per (strip, vector of channels).  Blocks
 // after them: sT, one thread per (sequence, vector of channels).
 template <typename IO, int VEC, int W>
@@ -127,7 +134,9 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 4)
     const int Cv = C / VEC;
     if (blockIdx.x >= blocks_rows) {
         const long i = static_cast<long>(blockIdx.x - blocks_rows) * kThreads + threadIdx.x;
-        if (i < static_cast<long>(B) * Cv)
+        if (!sT)
+            look_at_spans(offs, i, B, T, status);
+        else if (i < static_cast<long>(B) * Cv)
             write_state<IO, VEC, W>(x, ldx, s0, sT, offs, T, C, i / Cv, static_cast<int>(i % Cv) * VEC, status);
         return;
     }
@@ -423,6 +432,7 @@ __global__ void __launch_bounds__(kThreads)
     if (blockIdx.x >= sum_blocks) {
         const int Cv = C / VEC;
         const long i = static_cast<long>(blockIdx.x - sum_blocks) * kThreads + threadIdx.x;
+        if (!ds0) return look_at_spans(offs, i, B, T, status);
         if (i >= static_cast<long>(B) * Cv) return;
         const int c = static_cast<int>(i % Cv) * VEC;
         float wr[W][VEC], br[VEC];
@@ -453,6 +463,13 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kBwdStripRows = 32;  // the halo of W - 1 rows is read and worked on twice (16 rows: 27 us, 32: 24)
 constexpr long kWant = 512;
 
+// Blocks that take the sequences: a thread per vector of a state's channels, or per packed
+// sequence where no state is wanted.
+unsigned state_blocks(int B, int Cv, bool state, bool packed) {
+    const long n = state ? static_cast<long>(B) * Cv : packed ? B : 0;
+    return static_cast<unsigned>((n + kThreads - 1) / kThreads);
+}
+
 // True when VEC-element accesses at any row and at channel multiples of VEC are aligned.
 bool vec_ok(int vec, int C, long ld0, long ld1) { return C % vec == 0 && ld0 % vec == 0 && ld1 % vec == 0; }
 
@@ -467,7 +484,7 @@ cudaError_t fwd_typed(const ConvArgs& p, cudaStream_t st) {
     while (strip > 8 && (rows + strip - 1) / strip * Cv < 148L * kWant) strip >>= 1;
     const long strips = (rows + strip - 1) / strip;
     const unsigned nb = static_cast<unsigned>((strips * Cv + kThreads - 1) / kThreads);
-    const unsigned ns = p.sT ? static_cast<unsigned>((static_cast<long>(p.B) * Cv + kThreads - 1) / kThreads) : 0;
+    const unsigned ns = state_blocks(p.B, Cv, p.sT, p.seq_offsets);
     auto go = [&](unsigned blocks, unsigned blocks_rows) {
         if (blocks == 0) return;
         conv_fwd_kernel<IO, VEC, W><<<blocks, kThreads, 0, st>>>(
@@ -501,7 +518,7 @@ cudaError_t bwd_typed(const ConvBwdArgs& p, cudaStream_t st) {
              *dsT = static_cast<const IO*>(p.dsT);
     const int Cv = p.C / VEC;
     const unsigned sums = static_cast<unsigned>((static_cast<long>(W + 1) * p.C + kLanes - 1) / kLanes);
-    const unsigned states = p.ds0 ? static_cast<unsigned>((static_cast<long>(p.B) * Cv + kThreads - 1) / kThreads) : 0;
+    const unsigned states = state_blocks(p.B, Cv, p.ds0, p.seq_offsets);
     auto* tail = conv_bwd_tail_kernel<IO, VEC, W>;
     if (nblk == 0) {  // the call's only kernel: not to start before what the stream holds has ended
         tail<<<sums + states, kThreads, 0, st>>>(p.ws, p.dw, p.dbias, nblk, p.C, sums, x, p.ldx, p.w, p.bias, s0, dy,

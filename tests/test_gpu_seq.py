@@ -452,6 +452,24 @@ def test_bad_offsets_of_whole_sequences(wk, io, N, lens):
         assert torch.equal(sT[n], d["s0"][n]) and torch.equal(ds0[n], d["dsT"][n]), n
 
 
+def test_bad_offsets_of_a_convolution_without_states(wk):
+    """A bad pair between sequences that rows lead to is reported also where no state is wanted."""
+    x, w = torch.randn(64, 24, device="cuda"), torch.randn(24, 4, device="cuda")
+    for lens in ([0, 8, 4, 64], [0, 32, 16, 64], [0, 0, -3, 64]):
+        offs = torch.tensor(lens, dtype=torch.int32).cuda()
+        wk.wkv7_get_device_status()
+        wk.causal_conv(x, w, seq_offsets=offs, want_state=False)
+        assert wk.wkv7_get_device_status() == -6, lens
+        ws = torch.empty(wk.wkv7_causal_conv_backward_workspace_bytes(3, 64, 24, 4, True), dtype=torch.uint8, device="cuda")
+        wk.wkv7_causal_conv_backward(x, w, None, None, x.clone(), None, torch.empty_like(x), torch.empty_like(w), None, None,
+                                     ws, 3, 64, 24, 4, offs)
+        assert wk.wkv7_get_device_status() == -6, lens
+    offs = offsets([5, 0, 59]).cuda()
+    y, none = wk.causal_conv(x, w, seq_offsets=offs, want_state=False)
+    assert none is None and torch.equal(y, wk.causal_conv(x, w, seq_offsets=offs)[0])
+    assert wk.wkv7_get_device_status() == 0
+
+
 def test_scan_gradient_against_differences(wk):
     """<dy, y> + <dsT, sT> of the kernels along a random direction in every input: central
     differences with step h have a relative error of h^2 and noise of e32 / h; with
