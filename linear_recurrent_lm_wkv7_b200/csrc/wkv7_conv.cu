@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 4)
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) p = fmaf(wr[j][e], win[j][e], p);
                 const float v = in.get(e);
-                out[e] = act_f32(fmaf(wr[W - 1][e], v, p), act);
+                out[e] = act_f32<IO>(fmaf(wr[W - 1][e], v, p), act);
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
                 win[W - 2][e] = v;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
         float p = br[e];
 #pragma unroll
         for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], win[j][e], p);
-        out[e] = act_f32(p, act);
+        out[e] = act_f32<IO>(p, act);
     }
     store_vec<VEC>(y + n * ldy + c, out);
 #pragma unroll
@@ -261,7 +261,7 @@ __device__ void write_state_grad(const IO* x, long ldx, const IO* s0, const IO* 
             float p = br[e];
 #pragma unroll
             for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], row[t + j][e], p);
-            g[t][e] = t < len ? g[t][e] * act_grad_f32(p, act) : 0.f;
+            g[t][e] = t < len ? g[t][e] * act_grad_f32<IO>(p, act) : 0.f;
         }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float p = br[e];
 #pragma unroll
                     for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], xw[j][e], p);
-                    const float g = vg.get(e) * act_grad_f32(p, act);
+                    const float g = vg.get(e) * act_grad_f32<IO>(p, act);
                     gq[W - 1][e] = g;
                     if (count) {
 #pragma unroll

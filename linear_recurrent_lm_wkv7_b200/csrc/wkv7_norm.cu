@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads)
             if (p.lane + k * TEAM >= nv) continue;
             float out[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) out[e] = act_f32(fmaf(v[k][e] * rstd, wv[k][e], bv[k][e]), act);
+            for (int e = 0; e < VEC; ++e) out[e] = act_f32<IO>(fmaf(v[k][e] * rstd, wv[k][e], bv[k][e]), act);
             store_vec<VEC>(y + row * ldy + c0 + k * TEAM * VEC, out);
         }
     }
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 h[k][e] = (nx[k].get(e) - mean) * rstd;
-                q[k][e] = ny[k].get(e) * act_grad_f32(fmaf(h[k][e], wv[k][e], bv[k][e]), act);
+                q[k][e] = ny[k].get(e) * act_grad_f32<IO>(fmaf(h[k][e], wv[k][e], bv[k][e]), act);
                 ab[k][e] += q[k][e];
                 aw[k][e] = fmaf(q[k][e], h[k][e], aw[k][e]);
                 q[k][e] *= wv[k][e];
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads)
         float v[VEC];
         load_vec<VEC>(v, src + l * ldx);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = act_f32(fmaf((v[e] - st.x) * st.y, wv[e], bv[e]), act);
+        for (int e = 0; e < VEC; ++e) v[e] = act_f32<IO>(fmaf((v[e] - st.x) * st.y, wv[e], bv[e]), act);
         store_vec<VEC>(dst + l * ldy, v);
     }
 }
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 h[e] = (h[e] - mean) * rstd;
-                q[e] *= act_grad_f32(fmaf(h[e], wv[e], bv[e]), act);
+                q[e] *= act_grad_f32<IO>(fmaf(h[e], wv[e], bv[e]), act);
                 ab[e] += q[e];
                 aw[e] = fmaf(q[e], h[e], aw[e]);
             }
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             h[e] = (h[e] - mean) * rstd;
-            q[e] *= act_grad_f32(fmaf(h[e], wv[e], bv[e]), act) * wv[e];
+            q[e] *= act_grad_f32<IO>(fmaf(h[e], wv[e], bv[e]), act) * wv[e];
             q[e] = rstd * (q[e] - m1 - h[e] * m2);
         }
         store_vec<VEC>(dx + (n * L + l) * lddx + c, q);

@@ -609,6 +609,27 @@ def test_norm_constant_rows(wk):
     assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
 
 
+def test_silu_keeps_its_bits_far_out(wk):
+    """SiLU and its derivative, relative to their own size, from -85 to 85: a convolution whose
+    last tap is 1 and a norm without deviation hand the activation its argument as it is.
+    u s(u): exp 2^-22, the sum 2^-24, the division 2^-22 (2 ulp), the product 2^-24, which is
+    below 2^-20.5.  The derivative s (1 + u (1 - s)): s and 1 - s are off by 2^-21 of s and of 1,
+    so 2^-20 of s (1 + |u|)."""
+    u = torch.linspace(-85, 85, 8 * 4001, dtype=torch.float64).float()
+    x = u.view(1, 4001, 8).cuda()
+    w = torch.zeros(8, 4, device="cuda")
+    w[:, 3] = 1
+    s = torch.sigmoid(u.double())
+    y, _ = wk.causal_conv(x, w, act="silu")
+    dx, _, _, _ = wk.causal_conv_backward(x, w, torch.ones_like(x), act="silu")
+    ref, slope = u.double() * s, s * (1 + u.double() * (1 - s))
+    close("y", y.view(-1), ref, ref.abs(), 2.0 ** -20.5)
+    # rows of one value: h = 0, and the bias is the argument
+    z = wk.group_norm(torch.ones(1, u.numel(), device="cuda"), u.numel() // 8, None, u.cuda(), act="silu")
+    close("z", z[0], ref, ref.abs(), 2.0 ** -20.5)
+    close("dx", dx.view(-1), slope, s * (1 + u.double().abs()), 2.0 ** -20)
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_a_layer(wk, io):
