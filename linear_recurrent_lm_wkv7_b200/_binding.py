@@ -371,10 +371,15 @@ def _flat(t, name, dtype, shape, dev):
     return t.data_ptr()
 
 
+_INT = 2 ** 31 - 1  # the library's sizes are ints, and ctypes would cut larger ones
+
+
 def _rows(t, name, dtype, shape, lead, width, dev):
     """The pointer and the row stride of rows of ``width`` elements."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _wrong(t, name, dtype, shape, dev)
+    if shape[0] > _INT or shape[lead - 1] > _INT or width > _INT:
+        raise ValueError(f"{name}: every size must be below 2^31, not {tuple(shape)}")
     if lead == 1 and shape[0] > 1:  # the usual slice of a step or of packed rows
         st = t.stride()
         if st[-1] == 1 and (len(st) == 2 or st[1] == shape[2]):

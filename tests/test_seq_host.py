@@ -208,6 +208,16 @@ def test_python_refusals(wk):
         ld(torch.zeros(2, 8, 4, 80)[..., :64], 2, 256, "x")
 
 
+@pytest.mark.parametrize("shape,lead,width", [((2 ** 32 + 8, 1), 1, 1), ((2, 2 ** 32 + 8, 1), 2, 1), ((2 ** 31, 1, 1), 2, 1),
+                                              ((1, 2 ** 32 + 64), 1, 2 ** 32 + 64), ((2, 2, 2 ** 31), 2, 2 ** 31)])
+def test_sizes_past_the_library_s_are_refused(wk, shape, lead, width):
+    """The library counts in ints: a size that an int does not hold is refused, not cut to its
+    low bits (2^32 + 8 rows would be 8)."""
+    t = torch.empty(shape, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        wk._binding._rows(t, "x", t.dtype, t.shape, lead, width, t.get_device())
+
+
 def test_steps_mark_every_tensor_for_another_stream(wk, monkeypatch):
     """A step on a stream that is given marks its inputs, the state and y as used there, also
     where y is the caller's."""
