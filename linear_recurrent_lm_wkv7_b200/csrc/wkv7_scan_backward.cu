@@ -388,12 +388,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
         bulk_load(smem + off, a.states + (((back ? a.chunk_count : 0) + slot) * a.H + h) * (kStatePlanes * kState),
                   TS::bytes, bar);
     };
-    bool ok = true;  // a wait that gives up is reported, and is the last
+    // A wait that gives up is reported and is the last: it waits once more, so that no copy is on
+    // its way into shared memory when the block ends, and thread 0 starts no further one.
+    bool ok = true;
     uint32_t phase = 0;
     auto wait_states = [&]() {
         if (ok && !mbar_wait(bar, phase & 1, 2000000000ull)) {
             ok = false;
             report_status(a.status, WKV7_ERR_DEVICE_TIMEOUT);
+            mbar_wait(bar, phase & 1, 2000000000ull);
         }
         ++phase;
     };
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
         cp_async_commit();
     };
     auto load_states = [&](int i) {
-        if (tid != 0) return;
+        if (tid != 0 || !ok) return;
         mbar_arrive_expect_tx(bar, (LY::shared_state ? 1 : 2) * TS::bytes);
         load_state(LY::off_s0, 0, h0 + i);
         if constexpr (!LY::shared_state) load_state(LY::off_ds, 1, h0 + i);
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_grad_kernel(const BwdDev
         }
         if constexpr (LY::shared_state) {
             __syncthreads();  // S_0 has been read
-            if (tid == 0) {
+            if (tid == 0 && ok) {
                 mbar_arrive_expect_tx(bar, TS::bytes);
                 load_state(ods, 1, h0 + i);
             }
