@@ -8,8 +8,8 @@
 namespace wkv7 {
 
 // ---------------------------------------------------------------- vectors
-// VEC consecutive elements as floats, in accesses of 4, 8 or 16 bytes (VEC =
-// 2, 4 or 8, the address aligned to VEC elements) or element by element (VEC = 1).
+// VEC consecutive elements as floats, in accesses of 8 or 16 bytes (VEC = 4 or 8,
+// the address aligned to VEC elements) or element by element (VEC = 1).
 template <int VEC>
 __device__ __forceinline__ void load_vec(float (&f)[VEC], const __nv_bfloat16* p) {
     if constexpr (VEC == 8) {
@@ -24,11 +24,8 @@ __device__ __forceinline__ void load_vec(float (&f)[VEC], const __nv_bfloat16* p
         const uint2 u = *reinterpret_cast<const uint2*>(p);
         f[0] = __uint_as_float(u.x << 16), f[1] = __uint_as_float(u.x & 0xffff0000u);
         f[2] = __uint_as_float(u.y << 16), f[3] = __uint_as_float(u.y & 0xffff0000u);
-    } else if constexpr (VEC == 2) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-        f[0] = __uint_as_float(u << 16), f[1] = __uint_as_float(u & 0xffff0000u);
     } else {
-        static_assert(VEC == 1, "8, 4, 2 or 1 bf16");
+        static_assert(VEC == 1, "8, 4 or 1 bf16");
         f[0] = __bfloat162float(*p);
     }
 }
@@ -40,11 +37,8 @@ __device__ __forceinline__ void load_vec(float (&f)[VEC], const float* p) {
     } else if constexpr (VEC == 4) {
         const float4 u = *reinterpret_cast<const float4*>(p);
         f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-    } else if constexpr (VEC == 2) {
-        const float2 u = *reinterpret_cast<const float2*>(p);
-        f[0] = u.x, f[1] = u.y;
     } else {
-        static_assert(VEC == 1, "8, 4, 2 or 1 fp32");
+        static_assert(VEC == 1, "8, 4 or 1 fp32");
         f[0] = *p;
     }
 }
@@ -60,10 +54,8 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[VEC
                                                   pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
     } else if constexpr (VEC == 4) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
-    } else if constexpr (VEC == 2) {
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16(f[0], f[1]);
     } else {
-        static_assert(VEC == 1, "8, 4, 2 or 1 bf16");
+        static_assert(VEC == 1, "8, 4 or 1 bf16");
         *p = __float2bfloat16_rn(f[0]);
     }
 }
@@ -74,10 +66,8 @@ __device__ __forceinline__ void store_vec(float* p, const float (&f)[VEC]) {
         *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
     } else if constexpr (VEC == 4) {
         *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    } else if constexpr (VEC == 2) {
-        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
     } else {
-        static_assert(VEC == 1, "8, 4, 2 or 1 fp32");
+        static_assert(VEC == 1, "8, 4 or 1 fp32");
         *p = f[0];
     }
 }
