@@ -315,6 +315,26 @@ def test_scan_long_sequences_keep_their_sums(wk, io, N):
         close("dA", grads[2], dA.cpu(), dA.abs().cpu(), 2 * e + B * T * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("N", [16, 64, 128])
+def test_scan_in_fp32_sums_like_fp32(wk, N):
+    """A chunk of positive terms, where sums that are cut lose with one sign.  Each product of
+    matrices sums up to N / 16 = 8 steps in fp32 (2^-24 each), a step's six products cut at its
+    own size (2^-23): G or M 10 x 2^-24, the product with it (4 steps) 6 x 2^-24, the
+    exponential 2^-22, delta and the factors' roundings 12 x 2^-24: 32 x 2^-24 = 2^-19 in all."""
+    B, T, H = 2, 64, 2
+    inp = scan_inputs((B, T), B, H, N, 1, "f32", seed=N, state=False, skip=False, decay=(0.1, 0.5))
+    inp = {k: v if v is None or k == "A" else v.abs() for k, v in inp.items()}
+    inp["dt"] *= 0.1
+    names = ("x", "dt", "A", "Bm", "Cm")
+    ref = R.scan(*(inp[k] for k in names), softplus=True, dy=inp["dy"])
+    d = [cuda(inp[k]) for k in names]
+    out = dict(zip(("y", "sT"), wk.selective_scan(*d)))
+    grads = wk.selective_scan_backward(*d, inp["dy"].cuda())
+    out.update(dx=grads[0], dB=grads[3], dC=grads[4])
+    for k, v in out.items():
+        close(k, v, ref[k], ref[k], 2.0 ** -19)
+
+
 def test_calls_on_two_streams(wk):
     """The same kernels from two streams at once."""
     ins = []
