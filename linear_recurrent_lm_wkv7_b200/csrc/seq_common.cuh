@@ -84,30 +84,62 @@ template <typename IO>
 constexpr int kVec = 16 / static_cast<int>(sizeof(IO));
 
 // ---------------------------------------------------------------- activation
-// 1 / (1 + exp(-x)), for values of type IO.  exp(-x) overflows to +inf below x = -88, where the
-// quotient is 0, its limit.
-// The fast exponential rounds -x log2(e) to a float, so its relative error grows with |x| (2^-18
-// at x = -40): far below a bf16 result's rounding, 2^-9.  For fp32 results the rounding error of
-// that product goes in behind it (2^-21 for every x).
-// Convolution of fp32 B4 T4096 C2304: 61 us so and with the fast form; expf took 14 % longer (and
-// 25 % for bf16 B4 T1024 C2304).
+// 1 / (1 + exp(-x)).  exp(-x) overflows to +inf below x = -88, where the quotient is 0, its
+// limit; a subnormal exp(-x) counts as 0 beside the 1.
+// The rounding of -x log2(e) to a float is a relative error of 2^-24 |x| in the exponential
+// (2^-18 at x = -40): far below a bf16 result's rounding, 2^-9.  For fp32 results that rounding
+// error goes in behind the exponential (2^-21 for every x), two values an instruction where
+// registers allow it.  (Warm, in a graph: norm of fp32 [3][2111][960] 19.1 us, 18.3 without the
+// second part; convolution of fp32 B4 T4096 C2304 54.1 and 53.4, with expf 14 % longer.)
 template <typename IO>
-__device__ __forceinline__ float sigmoid_f32(float x) {
-    if constexpr (sizeof(IO) == 2) return __fdividef(1.f, 1.f + __expf(-x));
-    const float u = fminf(fmaxf(-x, -200.f), 200.f);  // no infinities: their products have no second part
+__device__ __forceinline__ float sigmoid_one(float x) {
+    if constexpr (sizeof(IO) == 2) return rcp_ftz(1.f + ex2_ftz(-1.44269504f * x));
+    const float u = fmaxf(-x, -200.f);  // of +inf there would be no second part; SiLU of -inf is NaN
     const float h = u * 1.44269504f, l = fmaf(u, 1.92596299e-8f, fmaf(u, 1.44269504f, -h));
-    return __fdividef(1.f, fmaf(ex2_ftz(h), fmaf(l, 0.69314718f, 1.f), 1.f));
+    return rcp_ftz(fmaf(ex2_ftz(h), fmaf(l, 0.69314718f, 1.f), 1.f));
+}
+__device__ __forceinline__ float2 sigmoid_pair(float2 x) {  // of fp32, the same bits
+    const float2 u = make_float2(fmaxf(-x.x, -200.f), fmaxf(-x.y, -200.f));
+    const float2 h = mul2(u, make_float2(1.44269504f, 1.44269504f));
+    const float2 r = fma2(u, make_float2(1.44269504f, 1.44269504f), make_float2(-h.x, -h.y));
+    const float2 l = fma2(u, make_float2(1.92596299e-8f, 1.92596299e-8f), r);
+    const float2 c = fma2(l, make_float2(0.69314718f, 0.69314718f), make_float2(1.f, 1.f));
+    const float2 n = fma2(make_float2(ex2_ftz(h.x), ex2_ftz(h.y)), c, make_float2(1.f, 1.f));
+    return make_float2(rcp_ftz(n.x), rcp_ftz(n.y));
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ void sigmoid_vec(float (&s)[VEC], const float (&x)[VEC]) {
+    if constexpr (sizeof(IO) == 2 || VEC == 1) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s[e] = sigmoid_one<IO>(x[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            const float2 v = sigmoid_pair(make_float2(x[e], x[e + 1]));
+            s[e] = v.x, s[e + 1] = v.y;
+        }
+    }
 }
 template <typename IO>
-__device__ __forceinline__ float act_f32(float x, int act) {
-    return act == WKV7_ACT_SILU ? x * sigmoid_f32<IO>(x) : x;
+__device__ __forceinline__ float act_one(float x, int act) {
+    return act == WKV7_ACT_SILU ? x * sigmoid_one<IO>(x) : x;
 }
-// d act(x) / dx
-template <typename IO>
-__device__ __forceinline__ float act_grad_f32(float x, int act) {
-    if (act != WKV7_ACT_SILU) return 1.f;
-    const float s = sigmoid_f32<IO>(x);
-    return s * (1.f + x * (1.f - s));
+template <typename IO, int VEC>
+__device__ __forceinline__ void act_vec(float (&x)[VEC], int act) {
+    if (act != WKV7_ACT_SILU) return;
+    float s[VEC];
+    sigmoid_vec<IO, VEC>(s, x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] *= s[e];
+}
+// g *= d act(x) / dx
+template <typename IO, int VEC>
+__device__ __forceinline__ void act_grad_vec(float (&g)[VEC], const float (&x)[VEC], int act) {
+    if (act != WKV7_ACT_SILU) return;
+    float s[VEC];
+    sigmoid_vec<IO, VEC>(s, x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[e] *= s[e] * (1.f + x[e] * (1.f - s[e]));
 }
 
 // ---------------------------------------------------------------- launches of one call

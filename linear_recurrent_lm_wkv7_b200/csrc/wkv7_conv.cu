@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 4)
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) p = fmaf(wr[j][e], win[j][e], p);
                 const float v = in.get(e);
-                out[e] = act_f32<IO>(fmaf(wr[W - 1][e], v, p), act);
+                out[e] = act_one<IO>(fmaf(wr[W - 1][e], v, p), act);
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
                 win[W - 2][e] = v;
@@ -214,8 +214,9 @@ __global__ void __launch_bounds__(kThreads)
         float p = br[e];
 #pragma unroll
         for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], win[j][e], p);
-        out[e] = act_f32<IO>(p, act);
+        out[e] = p;
     }
+    act_vec<IO, VEC>(out, act);
     store_vec<VEC>(y + n * ldy + c, out);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store_vec<VEC>(s_out + (n * (W - 1) + j) * C + c, win[j + 1]);
@@ -255,14 +256,18 @@ __device__ void write_state_grad(const IO* x, long ldx, const IO* s0, const IO* 
         }
     }
 #pragma unroll
-    for (int t = 0; t < W - 1; ++t)
+    for (int t = 0; t < W - 1; ++t) {
+        float p[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            float p = br[e];
+            p[e] = br[e];
 #pragma unroll
-            for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], row[t + j][e], p);
-            g[t][e] = t < len ? g[t][e] * act_grad_f32<IO>(p, act) : 0.f;
+            for (int j = 0; j < W; ++j) p[e] = fmaf(wr[j][e], row[t + j][e], p[e]);
         }
+        act_grad_vec<IO, VEC>(g[t], p, act);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[t][e] = t < len ? g[t][e] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         float d[VEC];
@@ -318,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             IO* pd = dx + r * lddx + c;
             // row u comes in; with COUNT it belongs to the strip
             auto step = [&](const Raw<IO, VEC>& vx, const Raw<IO, VEC>& vg, bool count) {
+                float p[VEC], g[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
 #pragma unroll
@@ -326,15 +332,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                         gq[j][e] = gq[j + 1][e];
                     }
                     xw[W - 1][e] = vx.get(e);
-                    float p = br[e];
+                    p[e] = br[e];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(wr[j][e], xw[j][e], p);
-                    const float g = vg.get(e) * act_grad_f32<IO>(p, act);
-                    gq[W - 1][e] = g;
+                    for (int j = 0; j < W; ++j) p[e] = fmaf(wr[j][e], xw[j][e], p[e]);
+                    g[e] = vg.get(e);
+                }
+                act_grad_vec<IO, VEC>(g, p, act);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    gq[W - 1][e] = g[e];
                     if (count) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) acc[j][e] = fmaf(g, xw[j][e], acc[j][e]);
-                        acc[W][e] += g;
+                        for (int j = 0; j < W; ++j) acc[j][e] = fmaf(g[e], xw[j][e], acc[j][e]);
+                        acc[W][e] += g[e];
                     }
                 }
             };

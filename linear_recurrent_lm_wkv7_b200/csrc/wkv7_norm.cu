@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kThreads)
             if (p.lane + k * TEAM >= nv) continue;
             float out[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) out[e] = act_f32<IO>(fmaf(v[k][e] * rstd, wv[k][e], bv[k][e]), act);
+            for (int e = 0; e < VEC; ++e) out[e] = fmaf(v[k][e] * rstd, wv[k][e], bv[k][e]);
+            act_vec<IO, VEC>(out, act);
             store_vec<VEC>(y + row * ldy + c0 + k * TEAM * VEC, out);
         }
     }
@@ -188,10 +189,16 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (!live || p.lane + k * TEAM >= nv) continue;
+            float pre[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 h[k][e] = (nx[k].get(e) - mean) * rstd;
-                q[k][e] = ny[k].get(e) * act_grad_f32<IO>(fmaf(h[k][e], wv[k][e], bv[k][e]), act);
+                pre[e] = fmaf(h[k][e], wv[k][e], bv[k][e]);
+                q[k][e] = ny[k].get(e);
+            }
+            act_grad_vec<IO, VEC>(q[k], pre, act);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
                 ab[k][e] += q[k][e];
                 aw[k][e] = fmaf(q[k][e], h[k][e], aw[k][e]);
                 q[k][e] *= wv[k][e];
@@ -412,13 +419,24 @@ __global__ void __launch_bounds__(kThreads)
     load_param<VEC>(bv, bias, c, 0.f);
     const IO* src = x + n * L * ldx + c;
     IO* dst = y + n * L * ldy + c;
-#pragma unroll 4
-    for (long l = l0 + prow; l < l1; l += par) {
+    auto row = [&](const Raw<IO, VEC>& in, long l) {
         float v[VEC];
-        load_vec<VEC>(v, src + l * ldx);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = act_f32<IO>(fmaf((v[e] - st.x) * st.y, wv[e], bv[e]), act);
+        for (int e = 0; e < VEC; ++e) v[e] = fmaf((in.get(e) - st.x) * st.y, wv[e], bv[e]);
+        act_vec<IO, VEC>(v, act);
         store_vec<VEC>(dst + l * ldy, v);
+    };
+    long l = l0 + prow;
+    Raw<IO, VEC> nx[4];
+    for (; l + 3 * par < l1; l += 4 * par) {  // four rows' loads before the first is used
+#pragma unroll
+        for (int u = 0; u < 4; ++u) nx[u].load(src + (l + u * par) * ldx);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) row(nx[u], l + u * par);
+    }
+    for (; l < l1; l += par) {
+        nx[0].load(src + l * ldx);
+        row(nx[0], l);
     }
 }
 
@@ -451,10 +469,15 @@ __global__ void __launch_bounds__(kThreads)
             float h[VEC], q[VEC];
             load_vec<VEC>(h, x + (n * L + l) * ldx + c);
             load_vec<VEC>(q, dy + (n * L + l) * lddy + c);
+            float pre[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 h[e] = (h[e] - mean) * rstd;
-                q[e] *= act_grad_f32<IO>(fmaf(h[e], wv[e], bv[e]), act);
+                pre[e] = fmaf(h[e], wv[e], bv[e]);
+            }
+            act_grad_vec<IO, VEC>(q, pre, act);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
                 ab[e] += q[e];
                 aw[e] = fmaf(q[e], h[e], aw[e]);
             }
@@ -528,12 +551,15 @@ __global__ void __launch_bounds__(kThreads)
         float h[VEC], q[VEC];
         load_vec<VEC>(h, x + (n * L + l) * ldx + c);
         load_vec<VEC>(q, dy + (n * L + l) * lddy + c);
+        float pre[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             h[e] = (h[e] - mean) * rstd;
-            q[e] *= act_grad_f32<IO>(fmaf(h[e], wv[e], bv[e]), act) * wv[e];
-            q[e] = rstd * (q[e] - m1 - h[e] * m2);
+            pre[e] = fmaf(h[e], wv[e], bv[e]);
         }
+        act_grad_vec<IO, VEC>(q, pre, act);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) q[e] = rstd * (q[e] * wv[e] - m1 - h[e] * m2);
         store_vec<VEC>(dx + (n * L + l) * lddx + c, q);
     }
 }
