@@ -339,7 +339,10 @@ int wkv7_backward_noalloc(const void* r, const void* w_log, const void* k, const
  *  - Outputs and workspaces must be disjoint from the inputs and from each other,
  *    except where a state may be updated in place.  Two row sets of one stride may
  *    interleave (columns of one buffer).
- *  - Sums, statistics, decays and states are fp32 or wider.
+ *  - Sums, statistics, decays and states are fp32 or wider.  The scan's matrix products take
+ *    their operands as sums of bf16 values: of three, a whole fp32, where fp32 inputs or
+ *    fp32 results are concerned; of two, 16 bits, where a result is rounded to bf16 (8
+ *    bits) at once.
  */
 typedef enum {
     WKV7_ACT_NONE = 0, /* act(u) = u */
@@ -396,7 +399,9 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
  * A dt of -inf leaves the state as it is (padding): x, Bm and Cm of such a token must
  * still be finite.  Prompts are worked on in chunks of 64 tokens (128 for bf16
  * with N = 128), so an infinity or NaN in x, Bm or Cm may reach the outputs of earlier
- * tokens of its chunk.  Rows are numbered in 31 bits: B T >= 2^31 is refused.
+ * tokens of its chunk.  An infinity among fp32 inputs, or a magnitude above 3.38e38, gives
+ * NaN also where the recurrence gives an infinity (its second and third bf16 parts are
+ * NaN).  Rows are numbered in 31 bits: B T >= 2^31 is refused.
  * wkv7_selective_scan_step: one token per sequence, B rows; s_out may be s_in (NULL:
  * zeros).
  * wkv7_selective_scan_backward: the gradient of <dy, y> + <dsT, sT>.
@@ -405,8 +410,8 @@ int wkv7_causal_conv_backward(const void* x, int64_t ld_x, const float* w, const
  *   over a group's heads), in the io dtype; dx, dB and dC need the alignment of x.
  *   dA : [H];  dD, ddt_bias : [H] or NULL (not wanted);  ds0 : [B][H][64][N] or NULL.
  *   workspace : at least wkv7_selective_scan_backward_workspace_bytes(B, T, H, D, N, G,
- *   io_dtype, packed) bytes (mostly the states and their gradients at every 64th
- *   token).  Sums are taken in a fixed order: equal calls give equal bits.  T == 0: the
+ *   io_dtype, packed) bytes: mostly the states and their gradients at every 64th
+ *   token, 12 N bytes a token and head (N = 128, 32768 tokens of 32 heads: 1.6 GB).  Sums are taken in a fixed order: equal calls give equal bits.  T == 0: the
  *   gradients of parameters are zero and ds0 receives dsT.
  */
 size_t wkv7_selective_scan_workspace_bytes(int B, int T, int H, int D, int N, int packed);

@@ -289,7 +289,9 @@ WKV7_ACT = {None: 0, "none": 0, "silu": 1}
 
 
 class _Runtime:
-    """What the calls use of torch, looked up once."""
+    """What the calls use of torch, looked up once.  The current stream is asked for by the name
+    that torch's own code generators use: 0.07 us, where ``torch.cuda.current_stream(dev).cuda_stream``
+    takes 1.3, of a call of 11."""
 
     def __init__(self):
         import torch

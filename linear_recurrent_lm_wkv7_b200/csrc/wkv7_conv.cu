@@ -11,10 +11,10 @@
 // channels.  Only the W - 1 rows above a strip are read twice (from L2).
 //
 // Measured: packed fp32 [16384][2307] W3 (a row stride that no vector divides, so accesses
-// of one element) 58.9 us, 5.1 TB/s; bf16 B4 T1024 C2304 W4 13.1 us, 2.9 TB/s, the tail of
-// a launch that short; a token of 256 sequences (C2816 W4) 6.7 us; gradients of B4 T1024
-// C2304 W4 25.5 us with the sums and ds0, where issue slots (activation, its derivative, four
-// windows) weigh as much as memory.
+// of one element) 61 us, 5.0 TB/s; bf16 B4 T1024 C2304 W4 12.6 us, 3.0 TB/s; a token of 256
+// sequences (C2816 W4) 6.6 us, most of it the filters, which every thread fetches for one row;
+// gradients of B4 T1024 C2304 W4 19.5 us and 3 for the sums and ds0: two blocks an SM of 128
+// registers a thread, waiting for loads, with half of the issue slots used.
 #include "seq_common.cuh"
 
 namespace wkv7 {
@@ -131,6 +131,9 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 4)
                     int T, long rows, int C, int act, int strip_rows, long strips, unsigned blocks_rows,
                     int* status) {
     constexpr int kAhead = kAheadOf<VEC>;
+    // vectors of fp32 leave no registers for a vector's activation at once (B4 T4096 C2304 W4: 63 us
+    // against 54 value by value; bf16 B4 T1024 C2304 9.7 us value by value, 9.5 at once)
+    constexpr bool kActOne = sizeof(IO) == 4 && VEC > 1;
     const int Cv = C / VEC;
     if (blockIdx.x >= blocks_rows) {
         const long i = static_cast<long>(blockIdx.x - blocks_rows) * kThreads + threadIdx.x;
@@ -166,11 +169,13 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 2 : 4)
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j) p = fmaf(wr[j][e], win[j][e], p);
                 const float v = in.get(e);
-                out[e] = act_one<IO>(fmaf(wr[W - 1][e], v, p), act);
+                out[e] = fmaf(wr[W - 1][e], v, p);
+                if constexpr (kActOne) out[e] = act_one<IO>(out[e], act);
 #pragma unroll
                 for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
                 win[W - 2][e] = v;
             }
+            if constexpr (!kActOne) act_vec<IO, VEC>(out, act);
             store_vec<VEC>(dst, out);
             dst += ldy;
         };

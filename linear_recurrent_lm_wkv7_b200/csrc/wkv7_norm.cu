@@ -16,9 +16,8 @@
 //   split form (any other size): partial sums per (sample, split of the rows), joined
 //              by a second pass that writes y.  x is read twice, the second time from
 //              L2 where it fits.
-// Measured: bf16 [4096][2048] in 32 groups 10.8 us (3.1 TB/s; half of it is the launch's
-// ramp and tail), its gradient 19 us + 3.2 for the sums; fp32 [3][2111][960] in 15 groups
-// 10.7 us for the sums and 10.6 for y, each a pass of 24 MB.
+// Measured: bf16 [4096][2048] in 32 groups 10.4 us (3.2 TB/s), its gradient 19.8 us + 3.2 for the
+// sums; fp32 [3][2111][960] in 15 groups 28.7 us, two passes over 24 MB.
 #include "seq_common.cuh"
 
 namespace wkv7 {
@@ -672,7 +671,7 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>(p.N) * s.splits, s.tiles);
     norm_stats_kernel<IO, VEC><<<grid, kThreads, 0, st>>>(x, p.ldx, part, p.L, p.C, Cg, s.lanes, s.splits, s.split_rows);
     // A launch less where the blocks can join the moments on the side: up to kJoinMost of
-    // them each (45 groups of 132 splits, fp32 [3][2111][960]: 21.4 us against 23 with a
+    // them each (45 groups of 99 splits, fp32 [3][2111][960]: 21.4 us against 23 with a
     // launch for the join).
     const int tile_groups = (s.lanes * VEC + Cg - 1) / Cg + 1;
     if (static_cast<long>(tile_groups) * s.splits * ((Cg + s.lanes * VEC - 1) / (s.lanes * VEC) + 1) <= kJoinMost) {

@@ -18,8 +18,8 @@
 //
 // What bounds it: no more than two blocks fit an SM, and their
 // warps wait for each other's results more than the tensor pipe is busy.  fp32, packed
-// [5003] rows in nine sequences, H12 N64 G4: decays 4 us, states 22, join 4, outputs 51, where
-// half of the tensor pipe's time is used (three planes of an operand: six products for one).
+// [5003] rows in nine sequences, H12 N64 G4: 86 us; of the outputs' 59 (ncu) the tensor pipe is
+// busy for 40 % (three planes of an operand: six products for one), of the states' 25 for 32 %.
 #include <algorithm>
 
 #include "scan_common.cuh"
@@ -485,9 +485,10 @@ constexpr CutCost kCutWarpF32{kChunk, 2, 1.7, 0.5, 0.5, 1.0}, kCutWarpF32Large{k
 const CutCost& cut_cost(int io_dtype, int N) {
     return io_dtype == WKV7_BF16 ? N == 128 ? kCutTc : kCutWarp : N == 128 ? kCutWarpF32Large : kCutWarpF32;
 }
-// bf16 with N = 128 runs on the tcgen05 kernel, whose tiles are 128 columns wide: B4 T1024 H32
-// takes 35 us there and took 114 on this file's.  Smaller N would leave those tiles half
-// empty or more, and fp32 rows would be three planes of each operand in its shared memory.
+// bf16 with N = 128 runs on the tcgen05 kernel: B4 T1024 H32 takes 35 us there and took 114 on this
+// file's.  It is written for tiles of 128 columns.  N = 64 takes 64 us here (96 with the L2
+// flushed), so even half-empty tiles of it would be faster there, which is not built; fp32 rows
+// would be three planes of each operand in its shared memory.
 bool uses_tc(int io_dtype, int N) { return io_dtype == WKV7_BF16 && N == 128; }
 
 template <typename IO, int N>
@@ -513,7 +514,7 @@ cudaError_t scan_typed(const ScanArgs& p, const SegMap& map, bool whole, ScanDev
 // Sequences are cut into segments where that is faster: blocks of one segment each run in
 // waves, and a cut needs a pass over the states and the join first.  Of packed sequences
 // only the mean length is known here; the longest is taken to have twice that.  (fp32
-// packed [5003] rows in nine sequences, H12 N64: 80 us in segments of four chunks, 145 whole.
+// packed [5003] rows in nine sequences, H12 N64: 86 us in segments of four chunks, 145 whole.
 // bf16 B4 T1024 H32 N64: 64 us whole, 74 in two segments; B1 T4096 H40 N64: 90 us in seven,
 // 115 in three.)
 SegMap scan_segments(int B, int T, int H, const int32_t* offs, bool packed, const CutCost& k) {
