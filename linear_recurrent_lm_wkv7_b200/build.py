@@ -21,7 +21,7 @@ SOURCES = ["wkv7_api.cu", "wkv7_decode.cu", "wkv7_prefill.cu", "wkv7_prefill_pip
            "wkv7_backward.cu", "wkv7_noalloc.cu", "wkv7_state.cu", "wkv7_seq_api.cu", "wkv7_conv.cu", "wkv7_scan.cu",
            "wkv7_scan_tc.cu", "wkv7_scan_backward.cu", "wkv7_norm.cu"]
 HEADERS = ["sm100_ptx.cuh", "wkv7_internal.cuh", "prefill_common.cuh", "tma_host.cuh", "seq_common.cuh",
-           "mma_common.cuh", "scan_common.cuh", "scan_backward.cuh"]
+           "mma_common.cuh", "packed_f32.cuh", "scan_common.cuh", "scan_backward.cuh"]
 
 
 def nvcc_path() -> str:

@@ -13,6 +13,7 @@
 #pragma once
 #include <cstdint>
 
+#include "packed_f32.cuh"
 #include "sm100_ptx.cuh"
 
 namespace wkv7 {

@@ -2,6 +2,7 @@
 // norm share: 16-byte vectors of either storage type, the activation and its
 // derivative, and the walk over packed sequences.
 #pragma once
+#include "packed_f32.cuh"
 #include "sm100_ptx.cuh"
 #include "wkv7_internal.cuh"
 

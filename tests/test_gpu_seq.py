@@ -650,6 +650,24 @@ def test_silu_keeps_its_bits_far_out(wk):
     close("dx", dx.view(-1), slope, s * (1 + u.double().abs()), 2.0 ** -20)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_silu_at_the_ends_of_the_range(wk, io):
+    """Arguments far past where the exponential overflows or vanishes: 0 or the argument; +inf
+    stays, NaN stays."""
+    u = torch.tensor([-3e38, -1e30, -1e9, -1e4, -200.0, 200.0, 1e4, 1e9, 1e30, 3e38, float("inf"), float("nan")]).to(DT[io])
+    want = torch.where(u < 0, torch.zeros_like(u), u)
+    rows = u.view(-1, 1, 1).expand(-1, 1, 8).contiguous().cuda()
+    w = torch.zeros(8, 4, device="cuda")
+    w[:, 3] = 1
+    y = wk.causal_conv(rows, w, act="silu")[0].cpu()
+    assert all(torch.equal(y[:, 0, c].nan_to_num(7.0, 9.0), want.nan_to_num(7.0, 9.0)) for c in range(8))
+    dx = wk.causal_conv_backward(rows[:10], w, torch.ones_like(rows[:10]), act="silu")[0].cpu()
+    assert torch.equal(dx[:, 0, 0].float(), (u[:10] > 0).float())
+    z = wk.group_norm(torch.ones(1, u.numel() * 8, dtype=DT[io], device="cuda"), u.numel(), None,
+                      u.float().repeat_interleave(8).cuda(), act="silu").cpu().view(-1, 8)
+    assert all(torch.equal(z[:, c].nan_to_num(7.0, 9.0), want.nan_to_num(7.0, 9.0)) for c in range(8))
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_a_layer(wk, io):
